@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libpace.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["pace_host.cpp", "pace_decode.hip", "pace_prefill.hip", "pace_baseline.hip", "pace_calib.hip"]
+SOURCES = ["pace_host.cpp", "pace_decode.hip", "pace_prefill.hip", "pace_baseline.hip", "pace_calib.hip",
+           "pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip"]
 # measurement kernels (include/pace_measure.h), a library of their own
 MEASURE_SOURCES = ["pace_measure.hip"]
 MEASURE_LIB = os.path.join(HERE, "libpace_measure.so")
@@ -33,16 +34,19 @@ COMMON = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # matrix-core results in ordinary VGPRs: no accumulator-register moves
     "-mllvm", "-amdgpu-mfma-vgpr-form",
-    # NaN / Inf inputs are undefined by the C ABI: min / max need no NaN quieting
-    "-fno-honor-nans",
     "-I" + os.path.join(ROOT, "include"),
 ]
+# NaN / Inf inputs are undefined by pace.h: min / max need no NaN quieting there.  The cache
+# and the attention over it (pace_cache.h) have defined results for them.
+FINITE_ONLY = ["-fno-honor-nans"]
+HONOR_NANS = {"pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip"}
 
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJ, os.path.splitext(src)[0] + ".o")
     lang = ["-x", "hip"] if src.endswith(".hip") else []
-    cmd = [HIPCC, *COMMON, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+    extra = [] if src in HONOR_NANS else FINITE_ONLY
+    cmd = [HIPCC, *COMMON, *extra, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
