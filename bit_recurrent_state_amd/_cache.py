@@ -14,8 +14,9 @@ from dataclasses import dataclass
 from functools import cached_property
 
 import numpy as np
+import torch
 
-from ._lib import IO_BF16, IO_F32, LIB, _check, _ptr, _stream
+from ._lib import IO_BF16, IO_F32, LIB, PACE_OK, PaceError, _check
 
 CACHE_KINDS = {"int8": 0, "int4": 1, "fp8": 2}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "blend": 3}
@@ -100,18 +101,42 @@ class CacheConfig:
 
 
 def _io(cfg):
-    import torch
     return torch.bfloat16 if cfg.bf16_io else torch.float32
 
 
-def _rows(t, name, dtype, lead, H, d):
-    """(pointer, token stride) of a tensor [*lead, H, d] whose tokens are evenly spaced."""
-    if not t.is_cuda:
+def _ptr(t, name, dtype, numel=None, optional=False):
+    """Address of a contiguous GPU tensor (None where an optional one is left out)."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (*lead, H, d):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    return t.data_ptr()
+
+
+def _stream(stream):
+    """The stream's handle; the current stream without building a Stream object for it (2.8 of
+    the 11 us that a call's host side took)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _rows(t, name, dtype, lead, H, d):
+    """(address, token stride) of a tensor [*lead, H, d] whose tokens are evenly spaced."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (*lead, H, d):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*lead, H, d)}")
+    if t.is_contiguous():
+        return t.data_ptr(), H * d
     st = t.stride()
     n = len(lead)
     if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
@@ -121,7 +146,7 @@ def _rows(t, name, dtype, lead, H, d):
         step = st[0] if n > 1 and lead[0] > 1 else H * d
     elif n > 1 and lead[0] > 1 and st[0] != lead[1] * step:
         raise ValueError(f"{name}: tokens must be evenly spaced over the sequences")
-    return ctypes.c_void_p(t.data_ptr()), step
+    return t.data_ptr(), step
 
 
 # ----------------------------------------------------------------------------- rotary
@@ -143,19 +168,19 @@ def rotary(cfg: RotaryConfig, positions, freqs, q, k, q_out, k_out, magnitude: f
            inverse: bool = False, stream=None):
     """pace_rotary.  q, q_out [n, Hq, d] and k, k_out [n, Hk, d] (None where the config has no
     heads of it; the output may be the input); positions int32 [n]; freqs fp64 [rd / 2]."""
-    import torch
     n = positions.numel()
-    io = _io(cfg)
-    args = []
-    for H, x, y, name in ((cfg.Hq, q, q_out, "q"), (cfg.Hk, k, k_out, "k")):
-        if H:
-            args.append((*_rows(x, name, io, (n,), H, cfg.d), *_rows(y, name + "_out", io, (n,), H, cfg.d)))
-        else:
-            args.append((None, 0, None, 0))
-    (qp, qs, qo, qos), (kp, ks, ko, kos) = args
-    _check(LIB.pace_rotary(ctypes.byref(cfg._c), n, _ptr(positions, "positions", torch.int32),
-                           _ptr(freqs, "freqs", torch.float64, cfg.rd // 2), magnitude, int(inverse),
-                           qp, qs, kp, ks, qo, qos, ko, kos, _stream(stream)), "pace_rotary")
+    io, lead, d = _io(cfg), (n,), cfg.d
+    qp = qo = kp = ko = None
+    qs = qos = ks = kos = 0
+    if cfg.Hq:
+        (qp, qs), (qo, qos) = _rows(q, "q", io, lead, cfg.Hq, d), _rows(q_out, "q_out", io, lead, cfg.Hq, d)
+    if cfg.Hk:
+        (kp, ks), (ko, kos) = _rows(k, "k", io, lead, cfg.Hk, d), _rows(k_out, "k_out", io, lead, cfg.Hk, d)
+    st = LIB.pace_rotary(ctypes.byref(cfg._c), n, _ptr(positions, "positions", torch.int32),
+                         _ptr(freqs, "freqs", torch.float64, cfg.rd // 2), magnitude, int(inverse),
+                         qp, qs, kp, ks, qo, qos, ko, kos, _stream(stream))
+    if st != PACE_OK:
+        raise PaceError(st, "pace_rotary")
 
 
 # ------------------------------------------------------------------------------ cache
@@ -168,7 +193,6 @@ def cache_layout(cfg: CacheConfig) -> dict:
 
 
 def _cache_io(fn, name, cfg, cache, page_table, positions, k, v, stream):
-    import torch
     if positions.dim() != 2 or positions.shape[0] != cfg.B:
         raise ValueError(f"positions has shape {tuple(positions.shape)}, expected ({cfg.B}, T)")
     T = positions.shape[1]
@@ -213,7 +237,6 @@ def cache_attention_workspace_bytes(cfg: CacheConfig, T: int, max_len: int) -> i
 
 
 def _attention_args(cfg, cache, page_table, q, ctx_lens, o, lse, tree, draft_lens, scale, max_len, workspace, stream):
-    import torch
     if q.dim() != 4:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected ({cfg.B}, T, {cfg.Hq}, {cfg.d})")
     T = q.shape[1]

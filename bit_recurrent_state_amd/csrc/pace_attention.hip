@@ -45,6 +45,14 @@ __device__ inline uint32_t pk_f16(float a, float b) {
   const half2_t h = {(_Float16)a, (_Float16)b};
   return u2(h);
 }
+// The rest of (a, b) after their fp16 rounding `hi`.  hi goes through an empty statement first, so
+// that the matrix operand and the subtraction see the same bits: without it the compiler forms the
+// operand with a fused multiply-and-round and the subtrahend with two roundings, which differ
+// by a unit where the product lies next to a tie.
+__device__ inline uint32_t pk_rest(float a, float b, uint32_t& hi) {
+  asm("" : "+v"(hi));
+  return pk_f16(a - (float)h2(hi)[0], b - (float)h2(hi)[1]);
+}
 __device__ inline float4_t mfma(half8_t a, half8_t b, float4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
@@ -209,8 +217,10 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnParams p) {
     // exponent field e of the maximum: |x| < 2^(e - 126); 2^(140 - e) takes it under 2^14
     int e = (int)(__float_as_uint(mx) >> 23) & 255;
     e = min(max(e, 14), 254);
-    const float up = __uint_as_float((uint32_t)min(140 - e + 127, 254) << 23);
-    cs[t] = p.scale_log2e / up;
+    float up = __uint_as_float((uint32_t)min(140 - e + 127, 254) << 23);
+    // scores are cs * (K q); the scale's sign goes into q, so that cs > 0 and masks can be -inf
+    cs[t] = p.scale_log2e == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2e) / up, 0x1p-126f);
+    up = p.scale_log2e == 0.f ? 0.f : copysignf(up, p.scale_log2e);
 #pragma unroll
     for (int G = 0; G < S::NB; ++G) {
       uint32_t w[4], z[4];
@@ -218,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnParams p) {
       for (int j = 0; j < 4; ++j) {
         const float a = x[G][2 * j] * up, c = x[G][2 * j + 1] * up;
         w[j] = pk_f16(a, c);
-        if constexpr (!BF16) z[j] = pk_f16(a - (float)h2(w[j])[0], c - (float)h2(w[j])[1]);
+        if constexpr (!BF16) z[j] = pk_rest(a, c, w[j]);
       }
       qf[0][t][G] = frag(w[0], w[1], w[2], w[3]);
       if constexpr (!BF16) qf[1][t][G] = frag(z[0], z[1], z[2], z[3]);
@@ -264,7 +274,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnParams p) {
       vs[u] = load_scales<S::NG>(v + rec.codes + (off[u] / 4 + g) * (S::NG * 8));
     }
 
-    // ---- scores: s[t][u][i] of token s0 + 16 u + 4 g + i and row n of tile t
+    // ---- scores over cs: s[t][u][i] of token s0 + 16 u + 4 g + i and row n of tile t
     float s[RT][2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -301,10 +311,6 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnParams p) {
           for (int t = 0; t < RT; ++t) s[t][u][i] = fmaf(a[t][i], k, s[t][u][i]);
         }
       }
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][u][i] *= cs[t];
     }
 
     // ---- masks, where some row may not see some token of the step
@@ -359,7 +365,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnParams p) {
       float x = fmaxf(s[t][0][0], s[t][0][1]);
       x = fmaxf(fmaxf(x, s[t][0][2]), s[t][0][3]);
       x = fmaxf(fmaxf(x, s[t][1][0]), s[t][1][1]);
-      mx[t] = rows_max(fmaxf(fmaxf(x, s[t][1][2]), s[t][1][3]));
+      mx[t] = rows_max(fmaxf(fmaxf(x, s[t][1][2]), s[t][1][3])) * cs[t];
       grow |= mx[t] > T[t].m + kLag;
     }
     if (__any(grow)) {
@@ -393,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnParams p) {
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[t][u][i] = __builtin_amdgcn_exp2f(s[t][u][i] - m);
+          s[t][u][i] = __builtin_amdgcn_exp2f(fmaf(s[t][u][i], cs[t], -m));   // one rounding, of the difference
           T[t].l += s[t][u][i];
         }
     }
@@ -419,8 +425,8 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnParams p) {
           w[2 * u] = pk_f16(x[0], x[o1]);
           w[2 * u + 1] = pk_f16(x[o2], x[3]);
           if constexpr (!BF16) {
-            z[2 * u] = pk_f16(x[0] - (float)h2(w[2 * u])[0], x[o1] - (float)h2(w[2 * u])[1]);
-            z[2 * u + 1] = pk_f16(x[o2] - (float)h2(w[2 * u + 1])[0], x[3] - (float)h2(w[2 * u + 1])[1]);
+            z[2 * u] = pk_rest(x[0], x[o1], w[2 * u]);
+            z[2 * u + 1] = pk_rest(x[o2], x[3], w[2 * u + 1]);
           }
         }
         pf[0][t] = frag(w[0], w[1], w[2], w[3]);

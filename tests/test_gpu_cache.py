@@ -591,3 +591,10 @@ def test_accepted_drafts_written_again_equal_a_plain_decode():
     s.cache = plain
     b = s.run(1, [42], q=q)
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+def test_attention_fp32_weights_keep_both_pieces_at_ties():
+    """Many rows over few tokens in fp32: one weight in some ten thousand lies next to a tie of
+    its fp16 piece, and its second piece has to match the first as the matrix unit got it."""
+    s = Scene(31, 24, 4, 4, 64, "fp8", 32, 16, [9] * 24, False)
+    s.check(6, [3] * 24)
