@@ -23,7 +23,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["pace_host.cpp", "pace_decode.hip", "pace_prefill.hip", "pace_baseline.hip", "pace_calib.hip",
-           "pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip"]
+           "pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip", "pace_attention_int8.hip",
+           "pace_attention_int4.hip", "pace_attention_fp8.hip"]
 # measurement kernels (include/pace_measure.h), a library of their own
 MEASURE_SOURCES = ["pace_measure.hip"]
 MEASURE_LIB = os.path.join(HERE, "libpace_measure.so")
@@ -39,7 +40,8 @@ COMMON = [
 # NaN / Inf inputs are undefined by pace.h: min / max need no NaN quieting there.  The cache
 # and the attention over it (pace_cache.h) have defined results for them.
 FINITE_ONLY = ["-fno-honor-nans"]
-HONOR_NANS = {"pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip"}
+HONOR_NANS = {"pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip", "pace_attention_int8.hip",
+              "pace_attention_int4.hip", "pace_attention_fp8.hip"}
 
 
 def _compile(src: str) -> str:
@@ -65,7 +67,7 @@ def _link(objs, lib):
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = SOURCES + MEASURE_SOURCES
-    with ThreadPoolExecutor(max_workers=min(4, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = dict(zip(srcs, ex.map(_compile, srcs)))
     _link([objs[s] for s in SOURCES], LIB)
     _link([objs[s] for s in MEASURE_SOURCES], MEASURE_LIB)

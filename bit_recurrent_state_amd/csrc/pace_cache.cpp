@@ -74,13 +74,14 @@ namespace pace {
 AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   AttnPlan a;
   const int64_t R = (int64_t)T * (c.Hq / c.Hkv);
-  a.row_tiles = 1;
+  a.row_tiles = c.d <= 128 && R > 16 ? 2 : 1;
   const int tiles = ceil_div(R, 16 * a.row_tiles);
   a.row_waves = tiles >= 3 ? 4 : tiles;
   a.row_blocks = ceil_div(tiles, a.row_waves);
-  const int step = 32 * (4 / a.row_waves);     // tokens all waves of a workgroup take at once
   const int64_t base = (int64_t)a.row_blocks * c.B * c.Hkv;
-  const int64_t want = std::max<int64_t>(1, 1024 / base);
+  a.waves = a.row_tiles == 1 && a.row_waves == 1 && base <= 256 && max_len <= 1024 ? 8 : 4;
+  const int step = 32 * (a.waves / a.row_waves);     // tokens all waves of a workgroup take at once
+  const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, 2048 / base);
   const int most = ceil_div(max_len, 2 * step);
   const int n = (int)std::min<int64_t>(want, most);
   a.chunk = ceil_div(ceil_div(max_len, n), step) * step;

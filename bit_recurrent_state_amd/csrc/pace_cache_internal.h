@@ -71,7 +71,8 @@ struct AttnParams {
 // How pace_cache_attention cuts its work (a function of host-known sizes only).
 struct AttnPlan {
   int32_t row_tiles;    // 16-row tiles a wave holds
-  int32_t row_waves;    // waves of a workgroup on different rows (4 / row_waves on tokens)
+  int32_t waves;        // of a workgroup: 4 or 8
+  int32_t row_waves;    // of them on different rows (the others on different tokens)
   int32_t row_blocks;   // workgroups over the rows
   int32_t nsplit, chunk;
 };
@@ -83,6 +84,12 @@ hipError_t launch_cache_write(const CacheIoParams& p, int kind, int d, int group
                               hipStream_t stream);
 hipError_t launch_cache_read(const CacheIoParams& p, int kind, int d, int group, int io_bf16,
                              hipStream_t stream);
+hipError_t launch_attention_int8(const AttnParams& p, const AttnPlan& plan, int d, int group, int io_bf16,
+                                 hipStream_t stream);
+hipError_t launch_attention_int4(const AttnParams& p, const AttnPlan& plan, int d, int group, int io_bf16,
+                                 hipStream_t stream);
+hipError_t launch_attention_fp8(const AttnParams& p, const AttnPlan& plan, int d, int group, int io_bf16,
+                                hipStream_t stream);
 hipError_t launch_attention(const AttnParams& p, const AttnPlan& plan, int kind, int d, int group,
                             int io_bf16, hipStream_t stream);
 

@@ -70,7 +70,8 @@ int main() {
     const int64_t rows = (int64_t)at_plan.row_blocks * at_plan.row_waves * at_plan.row_tiles * 16;
     EXPECT(rows >= at.R && rows - (int64_t)at_plan.row_waves * at_plan.row_tiles * 16 < at.R);
     EXPECT(at_plan.row_waves == 1 || at_plan.row_waves == 2 || at_plan.row_waves == 4);
-    EXPECT(at.nsplit >= 1 && at.chunk % (32 * (4 / at_plan.row_waves)) == 0);
+    EXPECT(at_plan.waves == 4 || at_plan.waves == 8);
+    EXPECT(at.nsplit >= 1 && at.chunk % (32 * (at_plan.waves / at_plan.row_waves)) == 0);
     EXPECT((int64_t)at.nsplit * at.chunk >= max_len && (int64_t)(at.nsplit - 1) * at.chunk < max_len);
     EXPECT((need != 0) == (at.nsplit > 1));
     if (need) {
