@@ -7,54 +7,91 @@
 namespace pace {
 namespace {
 
-constexpr int kJoinWaves = 4;
+constexpr int kJoin = 256;   // threads of a joining workgroup
 
-// Joins the pieces of a row: one wave a row, D / 64 channels a lane, pieces in order.
+// Joins the pieces of a row.  One workgroup a row: D / 4 threads hold its channels, four each, and
+// the 256 / (D / 4) groups of them take every so many-th piece, so that many pieces' loads are
+// in flight at once (one wave walking the pieces one by one took over 1 us a piece).  Weights
+// first, once, in LDS; sums in a fixed order.
 template <int D, bool BF16>
-__global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttnParams p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * kJoinWaves + (threadIdx.x >> 6);   // (b, h, r)
-  const int64_t rows = (int64_t)p.B * p.Hkv * p.R;
-  if (row >= rows) return;
-  constexpr int C = D / 64;
+__global__ __launch_bounds__(kJoin) void join_kernel(AttnParams p) {
+  constexpr int C = D / 4, NGRP = kJoin / C;
+  __shared__ float weight[kMaxPieces];
+  __shared__ float4 part[kJoin];
+  __shared__ float red[kJoin / 64][2];
+  const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.Hkv * p.R;   // (b, h, r)
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float top = -INFINITY;
-  for (int s = 0; s < p.nsplit; ++s) top = fmaxf(top, p.part_lse[s * rows + row]);
-  if (top == -INFINITY) top = 0.f;      // nothing seen (or NaN everywhere)
-  float acc[C] = {}, sum = 0.f;
-  for (int s = 0; s < p.nsplit; ++s) {
+  for (int s = threadIdx.x; s < p.nsplit; s += kJoin) {
     const float l = p.part_lse[s * rows + row];
-    if (l == -INFINITY) continue;       // an empty piece wrote no output
-    const float f = __builtin_amdgcn_exp2f(l - top);
-    sum += f;
-    const float* o = p.part_o + (s * rows + row) * D + lane * C;
+    weight[s] = l;
+    top = fmaxf(top, l);
+  }
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = fmaf(f, o[c], acc[c]);
+  for (int k = 1; k < 64; k *= 2) top = fmaxf(top, __shfl_xor(top, k));
+  if (lane == 0) red[wave][0] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
+  if (top == -INFINITY) top = 0.f;      // nothing seen (or NaN everywhere)
+  float sum = 0.f;
+  for (int s = threadIdx.x; s < p.nsplit; s += kJoin) {
+    const float f = __builtin_amdgcn_exp2f(weight[s] - top);
+    weight[s] = f;
+    sum += f;
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k *= 2) sum += __shfl_xor(sum, k);
+  if (lane == 0) red[wave][1] = sum;
+  __syncthreads();
+  sum = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
+  const int c = threadIdx.x % C, grp = threadIdx.x / C;
+  float4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = grp; s < p.nsplit; s += NGRP) {
+    const float f = weight[s];
+    if (f != 0.f) {                     // an empty piece wrote no output
+      const float4 o = *(const float4*)(p.part_o + (s * rows + row) * D + 4 * c);
+      acc.x = fmaf(f, o.x, acc.x);
+      acc.y = fmaf(f, o.y, acc.y);
+      acc.z = fmaf(f, o.z, acc.z);
+      acc.w = fmaf(f, o.w, acc.w);
+    }
+  }
+  part[threadIdx.x] = acc;
+  __syncthreads();
+  if (grp > 0) return;
+  for (int k = 1; k < NGRP; ++k) {
+    const float4 o = part[k * C + c];
+    acc.x += o.x;
+    acc.y += o.y;
+    acc.z += o.z;
+    acc.w += o.w;
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int r = (int)(row % p.R), i = r / p.gamma;
   const int64_t bh = row / p.R, b = bh / p.Hkv, h = bh % p.Hkv;
   const int64_t at = (b * p.T + i) * p.Hq + h * p.gamma + (r - i * p.gamma);
-  if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const float x = acc[c] * inv;
-    if constexpr (BF16)
-      ((uint16_t*)p.o)[at * D + lane * C + c] = __builtin_bit_cast(uint16_t, (__bf16)x);
-    else
-      ((float*)p.o)[at * D + lane * C + c] = x;
+  if (c == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+  if constexpr (BF16) {
+    auto pack = [&](float x, float y) {
+      return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(x * inv)) |
+             (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(y * inv)) << 16;
+    };
+    *(uint2*)((uint16_t*)p.o + at * D + 4 * c) = make_uint2(pack(acc.x, acc.y), pack(acc.z, acc.w));
+  } else {
+    *(float4*)((float*)p.o + at * D + 4 * c) = float4{acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
   }
 }
 
 template <bool BF16>
 hipError_t join(const AttnParams& p, int d, hipStream_t s) {
-  const int64_t rows = (int64_t)p.B * p.Hkv * p.R;
-  const uint32_t grid = (uint32_t)((rows + kJoinWaves - 1) / kJoinWaves);
+  const uint32_t grid = (uint32_t)((int64_t)p.B * p.Hkv * p.R);
   if (d == 64)
-    join_kernel<64, BF16><<<grid, kJoinWaves * 64, 0, s>>>(p);
+    join_kernel<64, BF16><<<grid, kJoin, 0, s>>>(p);
   else if (d == 128)
-    join_kernel<128, BF16><<<grid, kJoinWaves * 64, 0, s>>>(p);
+    join_kernel<128, BF16><<<grid, kJoin, 0, s>>>(p);
   else
-    join_kernel<256, BF16><<<grid, kJoinWaves * 64, 0, s>>>(p);
+    join_kernel<256, BF16><<<grid, kJoin, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -59,8 +59,9 @@ pace_status attn_sizes(const pace_cache_cfg* c, int32_t T, int32_t max_len, Attn
   const int64_t R = (int64_t)T * (c->Hq / c->Hkv);
   if (R > kMaxRows) return PACE_EUNSUPPORTED;
   *plan = attn_plan(*c, T, max_len);
+  // grids of the kernel and of the join
   const int64_t groups = (int64_t)plan->nsplit * plan->row_blocks * c->B * c->Hkv;
-  if (groups > INT32_MAX) return PACE_EUNSUPPORTED;
+  if (groups > INT32_MAX || (int64_t)c->B * c->Hkv * R > INT32_MAX) return PACE_EUNSUPPORTED;
   *bytes = plan->nsplit > 1
                ? (size_t)plan->nsplit * c->B * c->Hkv * (size_t)R * (size_t)(c->d + 1) * sizeof(float)
                : 0;
@@ -83,7 +84,7 @@ AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   const int step = 32 * (a.waves / a.row_waves);     // tokens all waves of a workgroup take at once
   const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, 2048 / base);
   const int most = ceil_div(max_len, 2 * step);
-  const int n = (int)std::min<int64_t>(want, most);
+  const int n = (int)std::min<int64_t>(std::min<int64_t>(want, most), kMaxPieces);
   a.chunk = ceil_div(ceil_div(max_len, n), step) * step;
   a.nsplit = ceil_div(max_len, a.chunk);
   return a;

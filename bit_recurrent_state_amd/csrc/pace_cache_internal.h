@@ -68,6 +68,8 @@ struct AttnParams {
   int32_t row_waves, row_blocks;
 };
 
+constexpr int kMaxPieces = 1024;   // of one context (the join keeps their weights in LDS)
+
 // How pace_cache_attention cuts its work (a function of host-known sizes only).
 struct AttnPlan {
   int32_t row_tiles;    // 16-row tiles a wave holds
