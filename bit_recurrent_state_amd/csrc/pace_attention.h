@@ -7,15 +7,19 @@
 // stored and their scales multiply the fp32 scores of a token.  Scores leave the instruction
 // with four consecutive tokens of one row in a lane, and the product O^T = V^T P^T takes
 // its eight tokens a lane in any order, so with values stored by quads of tokens the weights go
-// straight from registers back into the matrix unit: no LDS, no lane exchange but the row
-// maximum.  Value scales multiply the weights (they belong to a token and a channel group),
-// in units of a running power of two V >= every value scale seen, so that they fit fp16.
+// straight from registers back into the matrix unit: no lane exchange but the row maximum.
+// Value scales multiply the weights (they belong to a token and a channel group), in units of a
+// running power of two over every value scale seen, so that they fit fp16.
 // The softmax keeps a running maximum that may lag by kLag octaves (weights up to
 // 2^(kLift + kLag), which fp16 holds), so accumulators are rescaled only when it is exceeded.
 //
-// Work split: a workgroup's four waves take either different 16-row tiles of the same tokens
-// (row_waves) or different tokens of the same rows, joined in LDS at the end; long contexts are
-// also cut over workgroups, joined by a second kernel.
+// Two kernels (the choice is attn_plan's, by sizes):
+//   stream_kernel, for up to 32 rows: every wave takes other tokens for all rows, straight from
+//     memory into registers; the waves' results are joined in LDS.  Bound by the cache's bytes.
+//   tile_kernel, for more rows: every wave takes other rows; the workgroup unpacks each tile of
+//     tokens once, into LDS in operand order, for all four waves.  Bound by the vector unit (about
+//     nine operations a score) beside the matrix unit.
+// Long contexts are cut over workgroups, joined by a second kernel (pace_attention.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -31,8 +35,6 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
-
-constexpr int kStep = 32;        // tokens a wave takes at once
 
 constexpr float kLift = 7.f;     // weights are 2^kLift exp(s - m): fp16 stays normal down to 2^-21
 constexpr float kLag = 8.f;      // octaves the running maximum may lag behind
@@ -99,25 +101,23 @@ struct Codes {
     }
     return frag(w[0], w[1], w[2], w[3]);
   }
-  // channels 32 B + 2 n + {0, 1} of the lane's quads of both tiles
-  static __device__ void values(const uint32_t* v0, const uint32_t* v1, int B, uint32_t magic, half8_t (&f)[2]) {
+  // channels 32 B + 2 n + {0, 1} of the lane's quad of one tile: half of an operand each
+  static __device__ void value(const uint32_t* v, int B, uint32_t magic, uint2 (&f)[2]) {
     if constexpr (KIND == PACE_CACHE_INT4) {
-      uint32_t l[4], h[4];
-      two(v0[B], magic, l[0], h[0]);
-      two(v0[B] >> 8, magic, l[1], h[1]);
-      two(v1[B], magic, l[2], h[2]);
-      two(v1[B] >> 8, magic, l[3], h[3]);
-      f[0] = frag(l[0], l[1], l[2], l[3]);
-      f[1] = frag(h[0], h[1], h[2], h[3]);
+      two(v[B], magic, f[0].x, f[1].x);
+      two(v[B] >> 8, magic, f[0].y, f[1].y);
     } else {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t w[4];
-        four(v0[2 * B + e], w[0], w[1]);
-        four(v1[2 * B + e], w[2], w[3]);
-        f[e] = frag(w[0], w[1], w[2], w[3]);
-      }
+      four(v[2 * B], f[0].x, f[0].y);
+      four(v[2 * B + 1], f[1].x, f[1].y);
     }
+  }
+  // channels 32 B + 2 n + {0, 1} of the lane's quads of two tiles
+  static __device__ void values(const uint32_t* v0, const uint32_t* v1, int B, uint32_t magic, half8_t (&f)[2]) {
+    uint2 a[2], b[2];
+    value(v0, B, magic, a);
+    value(v1, B, magic, b);
+    f[0] = frag(a[0].x, a[0].y, b[0].x, b[0].y);
+    f[1] = frag(a[1].x, a[1].y, b[1].x, b[1].y);
   }
 };
 
@@ -176,172 +176,388 @@ __device__ inline float rows_sum(float x) {
   return __uint_as_float(a.lo) + __uint_as_float(a.hi);
 }
 __device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// Bit tests: these sources are compiled with NaNs not honoured in arithmetic, and a NaN row has
+// to stay one.
+__device__ inline bool is_zero(float x) { return __float_as_uint(x) == 0u; }
+__device__ inline bool is_empty(float lse) { return __float_as_uint(lse) == 0xFF800000u; }
 
 template <int KIND, int D, int GROUP, bool BF16>
 struct Shape {
   static constexpr int BITS = KIND == PACE_CACHE_INT4 ? 4 : 8;
-  static constexpr int LB = D * BITS / 32;      // bytes of a lane's codes
+  static constexpr int LB = D * BITS / 32;      // bytes of a lane's codes of a tile
   static constexpr int NB = D / 32;             // 32-channel blocks
   static constexpr int NG = D / GROUP;          // scale groups
   static constexpr int BPG = GROUP / 32;        // blocks a group
   static constexpr int PIECES = BF16 ? 1 : 2;   // fp16 pieces of q and of the weights
 };
 
-// Running state of one 16-row tile in a wave.
-template <int D>
-struct Tile {
-  float4_t acc[D / 16];   // [32 G + 2 (4 g + i) + e] of row lane % 16, at index 2 G + e, element i
-  float m, l;             // running maximum (base-2, all lanes of a row agree), sum of this lane
+// What a workgroup works on.
+struct Span {
+  int b, h, split, rb;   // sequence, key/value head, piece of the context, block of rows
+  int ctx, drafts;       // cached and drafted tokens of the sequence
+  int end;               // positions from here on are seen by no row of the workgroup
+  int lo, hi;            // its piece
+};
+__device__ inline Span span_of(const AttnParams& p, int rows) {
+  Span w;
+  int id = blockIdx.x;
+  w.split = id % p.nsplit;
+  id /= p.nsplit;
+  w.rb = id % p.row_blocks;
+  id /= p.row_blocks;
+  w.h = id % p.Hkv;
+  w.b = id / p.Hkv;
+  const int capacity = p.max_pages << p.page_shift;
+  w.ctx = min(max(p.ctx_lens[w.b], 0), capacity);
+  w.drafts = p.draft_lens ? min(max(p.draft_lens[w.b], 0), p.T) : p.T;
+  const int last_row = min((w.rb + 1) * rows, p.R) - 1;
+  const int seen = p.tree ? w.drafts : min(w.drafts, last_row / p.gamma + 1);
+  w.end = uniform(w.drafts > 0 ? (int)min((int64_t)w.ctx + seen, (int64_t)capacity) : 0);
+  w.lo = uniform(w.split * p.chunk);
+  w.hi = uniform(w.split == p.nsplit - 1 ? w.end : min(w.end, w.lo + p.chunk));
+  return w;
+}
+
+// A 16-token tile in memory; one past the end is replaced by the last (and masked).
+struct Place {
+  const uint8_t* at;   // the record
+  uint32_t off;        // its first token in the page
+  bool there;          // its page is one of the pool
+};
+__device__ inline Place place_of(const AttnParams& p, const Span& w, uint32_t record, int pos) {
+  const int tile = min(pos, max(w.end - 1, 0)) & ~15;
+  const int pg = uniform(p.table[(int64_t)w.b * p.max_pages + (tile >> p.page_shift)]);
+  Place r;
+  r.there = pg >= 0 && pg < p.num_pages;
+  r.at = p.cache + ((int64_t)(r.there ? pg : 0) * p.Hkv + w.h) * record;
+  r.off = (uint32_t)(tile & ((1 << p.page_shift) - 1));
+  return r;
+}
+
+// A wave's rows: RT tiles of 16, row n = lane % 16 of each, as matrix operands.
+template <class S, int RT>
+struct Rows {
+  half8_t q[S::PIECES][RT][S::NB];
+  float cs[RT];           // scores are cs * (K q)
+  int tok[RT];            // the row's token, or -1
+  const uint32_t* bits[RT];
+
+  __device__ void load(const AttnParams& p, const Span& w, int row0, int lane) {
+    const int n = lane & 15, g = lane >> 4;
+    constexpr int D = S::NB * 32;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int r = row0 + t * 16 + n, i = r / p.gamma;
+      tok[t] = (r < p.R && i < w.drafts) ? i : -1;
+      bits[t] = p.tree ? p.tree + (int64_t)w.b * p.tree_stride + (int64_t)max(tok[t], 0) * ((p.T + 31) / 32) : nullptr;
+      float x[S::NB][8];
+      float mx = 0.f;
+      const int64_t at = ((int64_t)w.b * p.T + max(tok[t], 0)) * p.q_stride +
+                         (int64_t)(w.h * p.gamma + (r - i * p.gamma)) * D + 8 * g;
+#pragma unroll
+      for (int B = 0; B < S::NB; ++B) {
+        if constexpr (S::PIECES == 1) {
+          const uint4 v = tok[t] >= 0 ? *(const uint4*)((const uint16_t*)p.q + at + 32 * B) : uint4{0, 0, 0, 0};
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[B][2 * j] = __uint_as_float(u[j] << 16);
+            x[B][2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float4 v = tok[t] >= 0 ? *(const float4*)((const float*)p.q + at + 32 * B + 4 * j) : float4{0, 0, 0, 0};
+            x[B][4 * j] = v.x; x[B][4 * j + 1] = v.y; x[B][4 * j + 2] = v.z; x[B][4 * j + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[B][j]));
+      }
+      mx = rows_max(mx);
+      // scaled by a power of two to [2^13, 2^14): exponent field e of the maximum says
+      // |x| < 2^(e - 126), and 2^(140 - e) takes it under 2^14
+      int e = (int)(__float_as_uint(mx) >> 23) & 255;
+      e = min(max(e, 14), 254);
+      float up = __uint_as_float((uint32_t)min(140 - e + 127, 254) << 23);
+      // the scale's sign goes into q, so that cs > 0 and masks can be -inf
+      cs[t] = p.scale_log2e == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2e) / up, 0x1p-126f);
+      up = p.scale_log2e == 0.f ? 0.f : copysignf(up, p.scale_log2e);
+#pragma unroll
+      for (int B = 0; B < S::NB; ++B) {
+        uint32_t u[4], z[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = x[B][2 * k] * up, c = x[B][2 * k + 1] * up;
+          u[k] = pk_f16(a, c);
+          if constexpr (S::PIECES == 2) z[k] = pk_rest(a, c, u[k]);
+        }
+        q[0][t][B] = frag(u[0], u[1], u[2], u[3]);
+        if constexpr (S::PIECES == 2) q[1][t][B] = frag(z[0], z[1], z[2], z[3]);
+      }
+    }
+  }
 };
 
+// Running softmax and outputs of a wave's rows.
+template <class S, int RT>
+struct Sums {
+  static constexpr int NJ = S::NB * 2;
+  float4_t acc[RT][NJ];   // [t][2 B + e][i]: channel 32 B + 2 (4 g + i) + e of row n
+  float m[RT], l[RT];     // running maximum (base 2, all lanes of a row agree), sum of this lane
+  float vunit, vinv;      // the running power of two over the value scales, its inverse
+
+  __device__ void clear() {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[t][j] = float4_t{0, 0, 0, 0};
+      m[t] = kFloor;
+      l[t] = 0.f;
+    }
+    vunit = vinv = 0.f;
+  }
+
+  // New maxima: s[t] holds scores over cs, vmax a bound of the step's value scales (all lanes).
+  template <int N>
+  __device__ void rescale(const float (&s)[RT][N], const float (&cs)[RT], float vmax) {
+    float mx[RT];
+    bool grow = vmax > vunit;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float x = s[t][0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) x = fmaxf(x, s[t][i]);
+      mx[t] = rows_max(x) * cs[t];
+      grow |= mx[t] > m[t] + kLag;
+    }
+    if (!__any(grow)) return;
+    float vf = 1.f;
+    if (vmax > vunit) {
+      // a power of two over vmax with two octaves to spare (value scales end at 2^125)
+      const uint32_t e = min((__float_as_uint(vmax) >> 23) + 3u, 253u);
+      const float now = __uint_as_float(e << 23);
+      vinv = __uint_as_float((254u - e) << 23);
+      vf = vunit * vinv;
+      vunit = now;
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const float now = fmaxf(m[t], mx[t]);
+      const float f = __builtin_amdgcn_exp2f(m[t] - now);
+      m[t] = now;
+      l[t] *= f;
+      const float both = f * vf;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][j][i] *= both;
+    }
+  }
+
+  // Scores become weights.
+  template <int N>
+  __device__ void weigh(float (&s)[RT][N], const float (&cs)[RT]) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const float base = m[t] - kLift;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], cs[t], -base));   // one rounding, of the difference
+        l[t] += s[t][i];
+      }
+    }
+  }
+
+  // This wave's outputs o = acc / l and the base-2 logarithms of the sums.
+  __device__ void finish(const int (&tok)[RT], float (&lse)[RT]) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float sum = rows_sum(l[t]);
+      if (tok[t] < 0) sum = 0.f;     // a row past the drafted tokens saw what it should not have
+      const float inv = is_zero(sum) ? 0.f : vunit / sum;
+      lse[t] = is_zero(sum) ? -INFINITY : m[t] - kLift + __builtin_amdgcn_logf(sum);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][j][i] *= inv;
+    }
+  }
+
+  // To memory: final rows, or this piece's part.
+  __device__ void store(const AttnParams& p, const Span& w, int row0, int lane, const float (&lse)[RT]) const {
+    constexpr int D = S::NB * 32;
+    const int n = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int r = row0 + t * 16 + n;
+      if (r >= p.R) continue;
+      const int i = r / p.gamma;
+      if (p.nsplit > 1) {
+        const int64_t at = ((int64_t)(w.split * p.B + w.b) * p.Hkv + w.h) * p.R + r;
+        if (g == 0) p.part_lse[at] = lse[t];
+        if (is_empty(lse[t])) continue;
+        float* o = p.part_o + at * D + 8 * g;
+#pragma unroll
+        for (int B = 0; B < S::NB; ++B) {
+          const float4_t a = acc[t][2 * B], c = acc[t][2 * B + 1];
+          *(float4*)(o + 32 * B) = float4{a[0], c[0], a[1], c[1]};
+          *(float4*)(o + 32 * B + 4) = float4{a[2], c[2], a[3], c[3]};
+        }
+      } else {
+        const int64_t at = ((int64_t)w.b * p.T + i) * p.Hq + w.h * p.gamma + (r - i * p.gamma);
+        if (g == 0 && p.lse) p.lse[at] = lse[t] * 0.69314718055994530942f;
+#pragma unroll
+        for (int B = 0; B < S::NB; ++B) {
+          const float4_t a = acc[t][2 * B], c = acc[t][2 * B + 1];
+          if constexpr (S::PIECES == 1) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __bf16 x = (__bf16)a[k], y = (__bf16)c[k];
+              u[k] = (uint32_t)__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16;
+            }
+            *(uint4*)((uint16_t*)p.o + at * D + 32 * B + 8 * g) = uint4{u[0], u[1], u[2], u[3]};
+          } else {
+            float* o = (float*)p.o + at * D + 32 * B + 8 * g;
+            *(float4*)o = float4{a[0], c[0], a[1], c[1]};
+            *(float4*)(o + 4) = float4{a[2], c[2], a[3], c[3]};
+          }
+        }
+      }
+    }
+  }
+};
+
+// -inf where row n of tile t may not see token pos = p0 + i (i < 4); held: the lane's tokens that
+// are there at all.
+template <class S, int RT, int N>
+__device__ inline void mask_scores(float (&s)[RT][N], int at, const AttnParams& p, const Span& w, const Rows<S, RT>& rows,
+                                   int p0, bool there) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pos = p0 + i, j = pos - w.ctx;
+    const bool held = there && pos < w.end;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      bool ok = held && rows.tok[t] >= 0;
+      if (ok && j >= 0) ok = p.tree ? (rows.bits[t][j >> 5] >> (j & 31)) & 1u : j <= rows.tok[t];
+      s[t][at + i] = ok ? s[t][at + i] : -INFINITY;
+    }
+  }
+}
+
+// Bytes of the lane's quad from p0 on that belong to tokens that are there.
+__device__ inline uint32_t held_bytes(const Span& w, int p0, bool there) {
+  const int n = there ? min(max(w.end - p0, 0), 4) : 0;
+  return n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+}
+
+// Old bytes may be NaN scales, or NaN codes of fp8, and 0 times NaN is NaN: values and their scales
+// of tokens that are not there become zero.
+template <int KIND, int LB, int NG>
+__device__ inline void drop_old(Raw<LB>& v, Scales<NG>& s, uint32_t keep) {
+  const uint32_t k01 = __builtin_amdgcn_perm(keep, keep, 0x01010000u), k23 = __builtin_amdgcn_perm(keep, keep, 0x03030202u);
+#pragma unroll
+  for (int G = 0; G < NG; ++G) {
+    s.w[G][0] &= k01;
+    s.w[G][1] &= k23;
+  }
+  if constexpr (KIND == PACE_CACHE_FP8) {
+#pragma unroll
+    for (int x = 0; x < LB / 4; ++x) v.w[x] &= keep;
+  }
+}
+
+// The weights of two tiles (scores at, at + 4) times their value scales, as matrix operands.
+template <class S, int KIND, int RT, int N>
+__device__ inline void weight_operands(const float (&s)[RT][N], int at, const float4_t (&sc)[2], half8_t (&pf)[S::PIECES][RT]) {
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    uint32_t w[4], z[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = s[t][at + 4 * u + i] * sc[u][i];
+      // the token order in which the value codes unpack
+      constexpr int o1 = KIND == PACE_CACHE_INT4 ? 2 : 1, o2 = 3 - o1;
+      w[2 * u] = pk_f16(x[0], x[o1]);
+      w[2 * u + 1] = pk_f16(x[o2], x[3]);
+      if constexpr (S::PIECES == 2) {
+        z[2 * u] = pk_rest(x[0], x[o1], w[2 * u]);
+        z[2 * u + 1] = pk_rest(x[o2], x[3], w[2 * u + 1]);
+      }
+    }
+    pf[0][t] = frag(w[0], w[1], w[2], w[3]);
+    if constexpr (S::PIECES == 2) pf[1][t] = frag(z[0], z[1], z[2], z[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------- stream_kernel
+
 template <int KIND, int D, int GROUP, bool BF16, int RT, int NW>
-__global__ __launch_bounds__(NW * 64) void attn_kernel(AttnParams p) {
+__global__ __launch_bounds__(NW * 64) void stream_kernel(AttnParams p) {
   using S = Shape<KIND, D, GROUP, BF16>;
   using C = Codes<KIND>;
+  constexpr int NT = stream_tiles(S::BITS, D, RT), STEP = 16 * NT;
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-  int id = blockIdx.x;
-  const int split = id % p.nsplit;
-  id /= p.nsplit;
-  const int rb = id % p.row_blocks;
-  id /= p.row_blocks;
-  const int h = id % p.Hkv, b = id / p.Hkv;
-  const int rw = wave % p.row_waves, tw = wave / p.row_waves, nt = NW / p.row_waves;
-  const int row0 = (rb * p.row_waves + rw) * (RT * 16);
+  const Span w = span_of(p, RT * 16);
+  const int row0 = w.rb * (RT * 16);
+  const CacheRecord rec = cache_record(D, GROUP, 1 << p.page_shift, S::BITS);
 
-  const int page = 1 << p.page_shift;
-  const CacheRecord rec = cache_record(D, GROUP, page, S::BITS);
-  const int capacity = p.max_pages << p.page_shift;
-  const int ctx = min(max(p.ctx_lens[b], 0), capacity);
-  const int drafts = p.draft_lens ? min(max(p.draft_lens[b], 0), p.T) : p.T;
-  // the last position any row of this workgroup can see, + 1
-  const int last_row = min((rb + 1) * p.row_waves * RT * 16, p.R) - 1;
-  const int seen = p.tree ? drafts : min(drafts, last_row / p.gamma + 1);
-  const int end = uniform(drafts > 0 ? (int)min((int64_t)ctx + seen, (int64_t)capacity) : 0);
-  const int lo = uniform(split * p.chunk), hi = uniform(split == p.nsplit - 1 ? end : min(end, lo + p.chunk));
-
-  // ---- the step's two 16-token tiles; a tile past the end is replaced and masked
-  const int32_t* table = p.table + (int64_t)b * p.max_pages;
-  const int last_tile = uniform(max(end - 1, 0) >> 4);
+  Raw<S::LB> kr[NT], vr[NT];
+  Scales<S::NG> ks[NT], vs[NT];
   struct Where {
-    const uint8_t* at[2];
-    uint32_t off[2];
-    bool there[2];
+    Place t[NT];
   };
   auto where = [&](int s0) {
-    Where w;
+    Where x;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int tile = min((s0 >> 4) + u, last_tile);
-      const int pg = uniform(table[(tile << 4) >> p.page_shift]);
-      w.there[u] = pg >= 0 && pg < p.num_pages;
-      w.at[u] = p.cache + ((int64_t)(w.there[u] ? pg : 0) * p.Hkv + h) * rec.total;
-      w.off[u] = (uint32_t)((tile << 4) & (page - 1));
-    }
-    return w;
+    for (int u = 0; u < NT; ++u) x.t[u] = place_of(p, w, rec.total, s0 + 16 * u);
+    return x;
   };
-  Raw<S::LB> kr[2], vr[2];
-  Scales<S::NG> ks[2], vs[2];
   // use == 0 (no further step): every lane asks for the tile's first bytes, one cache line
-  auto load_keys = [&](const Where& w, int use) {
+  auto load_keys = [&](const Where& x, int use) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      kr[u] = load_raw<S::LB, 64>(w.at[u] + w.off[u] * (D * S::BITS / 8), lane & use);
-      ks[u] = load_scales<S::NG>(w.at[u] + rec.codes + (w.off[u] / 4 + (g & use)) * (S::NG * 8));
+    for (int u = 0; u < NT; ++u) {
+      kr[u] = load_raw<S::LB, 64>(x.t[u].at + x.t[u].off * (D * S::BITS / 8), lane & use);
+      ks[u] = load_scales<S::NG>(x.t[u].at + rec.codes + (x.t[u].off / 4 + (g & use)) * (S::NG * 8));
     }
   };
-  auto load_values = [&](const Where& w, int use) {
+  auto load_values = [&](const Where& x, int use) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint8_t* v = w.at[u] + rec.codes + rec.scales;
-      vr[u] = load_raw<S::LB, 16>(v + (w.off[u] / 4 + (g & use)) * (D * S::BITS / 2), n & use);
-      vs[u] = load_scales<S::NG>(v + rec.codes + (w.off[u] / 4 + (g & use)) * (S::NG * 8));
+    for (int u = 0; u < NT; ++u) {
+      const uint8_t* v = x.t[u].at + rec.codes + rec.scales;
+      vr[u] = load_raw<S::LB, 16>(v + (x.t[u].off / 4 + (g & use)) * (D * S::BITS / 2), n & use);
+      vs[u] = load_scales<S::NG>(v + rec.codes + (x.t[u].off / 4 + (g & use)) * (S::NG * 8));
     }
   };
-  const int first = lo + tw * kStep, stride = nt * kStep;
+  const int first = w.lo + wave * STEP;
+  constexpr int stride = NW * STEP;
   Where cur;
-  if (first < hi) {
+  if (first < w.hi) {
     cur = where(first);
     load_keys(cur, -1);
     load_values(cur, -1);
   }
-
-  // ---- the rows' queries as fp16 operands, scaled by a power of two to [2^13, 2^14)
-  half8_t qf[S::PIECES][RT][S::NB];
-  float cs[RT];
-  int tok[RT];                 // the row's token, or -1
-  const uint32_t* bits[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int r = row0 + t * 16 + n, i = r / p.gamma;
-    tok[t] = (r < p.R && i < drafts) ? i : -1;
-    bits[t] = p.tree ? p.tree + (int64_t)b * p.tree_stride + (int64_t)max(tok[t], 0) * ((p.T + 31) / 32) : nullptr;
-    float x[S::NB][8];
-    float mx = 0.f;
-    const int64_t at = ((int64_t)b * p.T + max(tok[t], 0)) * p.q_stride + (int64_t)(h * p.gamma + (r - i * p.gamma)) * D + 8 * g;
-#pragma unroll
-    for (int G = 0; G < S::NB; ++G) {
-      if constexpr (BF16) {
-        const uint4 v = tok[t] >= 0 ? *(const uint4*)((const uint16_t*)p.q + at + 32 * G) : uint4{0, 0, 0, 0};
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[G][2 * j] = __uint_as_float(w[j] << 16);
-          x[G][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 v = tok[t] >= 0 ? *(const float4*)((const float*)p.q + at + 32 * G + 4 * j) : float4{0, 0, 0, 0};
-          x[G][4 * j] = v.x; x[G][4 * j + 1] = v.y; x[G][4 * j + 2] = v.z; x[G][4 * j + 3] = v.w;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[G][j]));
-    }
-    mx = rows_max(mx);
-    // exponent field e of the maximum: |x| < 2^(e - 126); 2^(140 - e) takes it under 2^14
-    int e = (int)(__float_as_uint(mx) >> 23) & 255;
-    e = min(max(e, 14), 254);
-    float up = __uint_as_float((uint32_t)min(140 - e + 127, 254) << 23);
-    // scores are cs * (K q); the scale's sign goes into q, so that cs > 0 and masks can be -inf
-    cs[t] = p.scale_log2e == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2e) / up, 0x1p-126f);
-    up = p.scale_log2e == 0.f ? 0.f : copysignf(up, p.scale_log2e);
-#pragma unroll
-    for (int B = 0; B < S::NB; ++B) {
-      uint32_t w[4], z[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float a = x[B][2 * k] * up, c = x[B][2 * k + 1] * up;
-        w[k] = pk_f16(a, c);
-        if constexpr (!BF16) z[k] = pk_rest(a, c, w[k]);
-      }
-      qf[0][t][B] = frag(w[0], w[1], w[2], w[3]);
-      if constexpr (!BF16) qf[1][t][B] = frag(z[0], z[1], z[2], z[3]);
-    }
-  }
-
-  Tile<D> T[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) T[t].acc[j] = float4_t{0, 0, 0, 0};
-    T[t].m = kFloor;
-    T[t].l = 0.f;
-  }
+  Rows<S, RT> rows;
+  rows.load(p, w, row0, lane);
+  Sums<S, RT> sums;
+  sums.clear();
   uint32_t magic = 0x64006400u;
   asm("" : "+v"(magic));
-  float vunit = 0.f, vinv = 0.f;   // the running power of two over the value scales, its inverse
 
-  for (int s0 = first; s0 < hi; s0 += stride) {
-    const bool more = s0 + stride < hi;
+  for (int s0 = first; s0 < w.hi; s0 += stride) {
+    const bool more = s0 + stride < w.hi;
     const int use = more ? -1 : 0;
     const Where next = where(more ? s0 + stride : s0);
 
-    // ---- scores over cs: s[t][u][i] of token s0 + 16 u + 4 g + i and row n of tile t
-    float s[RT][2][4];
+    // ---- scores over cs: s[t][4 u + i] of token s0 + 16 u + 4 g + i
+    float s[RT][4 * NT];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < NT; ++u) {
 #pragma unroll
       for (int G = 0; G < S::NG; ++G) {
         float4_t a[RT];
@@ -354,266 +570,318 @@ __global__ __launch_bounds__(NW * 64) void attn_kernel(AttnParams p) {
 #pragma unroll
           for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int c = 0; c < S::PIECES; ++c) a[t] = mfma(kf, qf[c][t][B], a[t]);
+            for (int c = 0; c < S::PIECES; ++c) a[t] = mfma(kf, rows.q[c][t][B], a[t]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float k = ks[u].get(G, i);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) s[t][u][i] = G == 0 ? a[t][i] * k : fmaf(a[t][i], k, s[t][u][i]);
+          for (int t = 0; t < RT; ++t) s[t][4 * u + i] = G == 0 ? a[t][i] * k : fmaf(a[t][i], k, s[t][4 * u + i]);
         }
       }
     }
     load_keys(next, use);
 
-    // ---- masks, where some row may not see some token of the step
-    if (s0 + kStep > ctx || !cur.there[0] || !cur.there[1]) {
+    bool there = true;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < NT; ++u) there = there && cur.t[u].there;
+    if (s0 + STEP > w.ctx || !there) {
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
         const int p0 = s0 + 16 * u + 4 * g;
-        uint32_t keep = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int pos = p0 + i;
-          const bool held = cur.there[u] && pos < end;
-          if (held) keep |= 0xFFu << (8 * i);
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const int j = pos - ctx;
-            bool ok = held && tok[t] >= 0;
-            if (ok && j >= 0) ok = p.tree ? (bits[t][j >> 5] >> (j & 31)) & 1u : j <= tok[t];
-            s[t][u][i] = ok ? s[t][u][i] : -INFINITY;
-          }
-        }
-        // old bytes may be NaN scales, or NaN codes of fp8, and 0 times NaN is NaN
-        const uint32_t k01 = __builtin_amdgcn_perm(keep, keep, 0x01010000u), k23 = __builtin_amdgcn_perm(keep, keep, 0x03030202u);
-#pragma unroll
-        for (int G = 0; G < S::NG; ++G) {
-          vs[u].w[G][0] &= k01;
-          vs[u].w[G][1] &= k23;
-        }
-        if constexpr (KIND == PACE_CACHE_FP8) {
-#pragma unroll
-          for (int x = 0; x < S::LB / 4; ++x) vr[u].w[x] &= keep;
-        }
+        mask_scores<S>(s, 4 * u, p, w, rows, p0, cur.t[u].there);
+        drop_old<KIND>(vr[u], vs[u], held_bytes(w, p0, cur.t[u].there));
       }
     }
 
-    // ---- running maximum and value unit; rescale when either is exceeded
-    // (scales are not negative: their bf16 patterns compare as integers, two at a time)
+    // scales are not negative: their bf16 patterns compare as integers, two at a time
     ushort2_t top = us2(vs[0].w[0][0]);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
       for (int G = 0; G < S::NG; ++G)
 #pragma unroll
         for (int i = 0; i < 2; ++i) top = __builtin_elementwise_max(top, us2(vs[u].w[G][i]));
-    const float vmax = rows_max(__uint_as_float((uint32_t)max(top[0], top[1]) << 16));
-    float mx[RT];
-    bool grow = vmax > vunit;
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      float x = fmaxf(s[t][0][0], s[t][0][1]);
-      x = fmaxf(fmaxf(x, s[t][0][2]), s[t][0][3]);
-      x = fmaxf(fmaxf(x, s[t][1][0]), s[t][1][1]);
-      mx[t] = rows_max(fmaxf(fmaxf(x, s[t][1][2]), s[t][1][3])) * cs[t];
-      grow |= mx[t] > T[t].m + kLag;
-    }
-    if (__any(grow)) {
-      float vf = 1.f;
-      if (vmax > vunit) {
-        // a power of two over vmax with two octaves to spare (value scales end at 2^125)
-        const uint32_t e = min((__float_as_uint(vmax) >> 23) + 3u, 253u);
-        const float now = __uint_as_float(e << 23);
-        vinv = __uint_as_float((254u - e) << 23);
-        vf = vunit * vinv;
-        vunit = now;
-      }
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const float now = fmaxf(T[t].m, mx[t]);
-        const float f = __builtin_amdgcn_exp2f(T[t].m - now);
-        T[t].m = now;
-        T[t].l *= f;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) T[t].acc[j][i] *= f * vf;
-      }
-    }
+    sums.rescale(s, rows.cs, rows_max(__uint_as_float((uint32_t)max(top[0], top[1]) << 16)));
+    sums.weigh(s, rows.cs);
 
-    // ---- weights, and O^T += V^T P^T
+    // ---- O^T += V^T P^T
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const float m = T[t].m - kLift;
+    for (int pr = 0; pr < NT / 2; ++pr)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int G = 0; G < S::NG; ++G) {
+        float4_t sc[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[t][u][i] = __builtin_amdgcn_exp2f(fmaf(s[t][u][i], cs[t], -m));   // one rounding, of the difference
-          T[t].l += s[t][u][i];
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[u][i] = vs[2 * pr + u].get(G, i) * sums.vinv;
+        half8_t pf[S::PIECES][RT];
+        weight_operands<S, KIND>(s, 8 * pr, sc, pf);
+#pragma unroll
+        for (int jb = 0; jb < S::BPG; ++jb) {
+          const int B = G * S::BPG + jb;
+          half8_t vf[2];
+          C::values(vr[2 * pr].w, vr[2 * pr + 1].w, B, magic, vf);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+              for (int c = 0; c < S::PIECES; ++c) sums.acc[t][2 * B + e] = mfma(vf[e], pf[c][t], sums.acc[t][2 * B + e]);
         }
-    }
-#pragma unroll
-    for (int G = 0; G < S::NG; ++G) {
-      half8_t pf[S::PIECES][RT];
-      float sc[2][4];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[u][i] = vs[u].get(G, i) * vinv;
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        uint32_t w[4], z[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = s[t][u][i] * sc[u][i];
-          // the token order in which the value codes unpack
-          constexpr int o1 = KIND == PACE_CACHE_INT4 ? 2 : 1, o2 = 3 - o1;
-          w[2 * u] = pk_f16(x[0], x[o1]);
-          w[2 * u + 1] = pk_f16(x[o2], x[3]);
-          if constexpr (!BF16) {
-            z[2 * u] = pk_rest(x[0], x[o1], w[2 * u]);
-            z[2 * u + 1] = pk_rest(x[o2], x[3], w[2 * u + 1]);
-          }
-        }
-        pf[0][t] = frag(w[0], w[1], w[2], w[3]);
-        if constexpr (!BF16) pf[1][t] = frag(z[0], z[1], z[2], z[3]);
       }
-#pragma unroll
-      for (int jb = 0; jb < S::BPG; ++jb) {
-        const int B = G * S::BPG + jb;
-        half8_t vf[2];
-        C::values(vr[0].w, vr[1].w, B, magic, vf);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int c = 0; c < S::PIECES; ++c) T[t].acc[2 * B + e] = mfma(vf[e], pf[c][t], T[t].acc[2 * B + e]);
-      }
-    }
     load_values(next, use);
     cur = next;
   }
 
-  // ---- this wave's result: o = acc V / l of its tokens, base-2 log of the sum
   float lse[RT];
+  sums.finish(rows.tok, lse);
+
+  // ---- joined over the waves
+  constexpr int REGS = D / 4;   // accumulator registers of a tile
+  constexpr int SLOT = RT * (REGS + 1) * 64;
+  if (wave > 0) {
+    float* mine = lds + (size_t)(wave - 1) * SLOT;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine[(t * (REGS + 1) + 4 * j + i) * 64 + lane] = sums.acc[t][j][i];
+      mine[(t * (REGS + 1) + REGS) * 64 + lane] = lse[t];
+    }
+  }
+  __syncthreads();
+  if (wave > 0) return;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    float l = rows_sum(T[t].l);
-    if (tok[t] < 0) l = 0.f;     // a row past the drafted tokens saw what it should not have
-    const float inv = l == 0.f ? 0.f : vunit / l;      // a NaN row stays NaN
-    lse[t] = l == 0.f ? -INFINITY : T[t].m - kLift + __builtin_amdgcn_logf(l);
+    float top = lse[t];
+    for (int k = 1; k < NW; ++k) top = fmaxf(top, lds[(size_t)(k - 1) * SLOT + (t * (REGS + 1) + REGS) * 64 + lane]);
+    const float base = is_empty(top) ? 0.f : top;
+    float f = __builtin_amdgcn_exp2f(lse[t] - base), sum = f;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) T[t].acc[j][i] *= inv;
-  }
-
-  // ---- joined over the waves that took other tokens of the same rows
-  if (nt > 1) {
-    constexpr int REGS = D / 4;   // accumulator registers of a tile
-    constexpr int SLOT = RT * (REGS + 1) * 64;
-    if (tw > 0) {
-      float* mine = lds + (size_t)((tw - 1) * p.row_waves + rw) * SLOT;
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mine[(t * (REGS + 1) + 4 * j + i) * 64 + lane] = T[t].acc[j][i];
-        mine[(t * (REGS + 1) + REGS) * 64 + lane] = lse[t];
-      }
-    }
-    __syncthreads();
-    if (tw > 0) return;
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      float top = lse[t];
-      for (int w = 1; w < nt; ++w)
-        top = fmaxf(top, lds[(size_t)((w - 1) * p.row_waves + rw) * SLOT + (t * (REGS + 1) + REGS) * 64 + lane]);
-      const float base = top == -INFINITY ? 0.f : top;
-      float f = __builtin_amdgcn_exp2f(lse[t] - base), sum = f;
+      for (int i = 0; i < 4; ++i) sums.acc[t][j][i] *= f;
+    for (int k = 1; k < NW; ++k) {
+      const float* from = lds + (size_t)(k - 1) * SLOT + t * (REGS + 1) * 64 + lane;
+      f = __builtin_amdgcn_exp2f(from[REGS * 64] - base);
+      sum += f;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) T[t].acc[j][i] *= f;
-      for (int w = 1; w < nt; ++w) {
-        const float* from = lds + (size_t)((w - 1) * p.row_waves + rw) * SLOT + t * (REGS + 1) * 64 + lane;
-        f = __builtin_amdgcn_exp2f(from[REGS * 64] - base);
-        sum += f;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) T[t].acc[j][i] = fmaf(from[(4 * j + i) * 64], f, T[t].acc[j][i]);
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      lse[t] = sum == 0.f ? -INFINITY : base + __builtin_amdgcn_logf(sum);
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) T[t].acc[j][i] *= inv;
+        for (int i = 0; i < 4; ++i) sums.acc[t][j][i] = fmaf(from[(4 * j + i) * 64], f, sums.acc[t][j][i]);
     }
+    const float inv = is_zero(sum) ? 0.f : 1.f / sum;
+    lse[t] = is_zero(sum) ? -INFINITY : base + __builtin_amdgcn_logf(sum);
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sums.acc[t][j][i] *= inv;
   }
-
-  // ---- out: final rows, or this piece's part
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int r = row0 + t * 16 + n;
-    if (r >= p.R) continue;
-    const int i = r / p.gamma;
-    if (p.nsplit > 1) {
-      const int64_t at = ((int64_t)(split * p.B + b) * p.Hkv + h) * p.R + r;
-      if (g == 0) p.part_lse[at] = lse[t];
-      if (lse[t] == -INFINITY) continue;
-      float* o = p.part_o + at * D + 8 * g;
-#pragma unroll
-      for (int G = 0; G < S::NB; ++G) {
-        const float4_t a = T[t].acc[2 * G], c = T[t].acc[2 * G + 1];
-        *(float4*)(o + 32 * G) = float4{a[0], c[0], a[1], c[1]};
-        *(float4*)(o + 32 * G + 4) = float4{a[2], c[2], a[3], c[3]};
-      }
-    } else {
-      const int64_t at = ((int64_t)b * p.T + i) * p.Hq + h * p.gamma + (r - i * p.gamma);
-      if (g == 0 && p.lse) p.lse[at] = lse[t] * 0.69314718055994530942f;
-#pragma unroll
-      for (int G = 0; G < S::NB; ++G) {
-        const float4_t a = T[t].acc[2 * G], c = T[t].acc[2 * G + 1];
-        if constexpr (BF16) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __bf16 x = (__bf16)a[k], y = (__bf16)c[k];
-            w[k] = (uint32_t)__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16;
-          }
-          *(uint4*)((uint16_t*)p.o + at * D + 32 * G + 8 * g) = uint4{w[0], w[1], w[2], w[3]};
-        } else {
-          float* o = (float*)p.o + at * D + 32 * G + 8 * g;
-          *(float4*)o = float4{a[0], c[0], a[1], c[1]};
-          *(float4*)(o + 4) = float4{a[2], c[2], a[3], c[3]};
-        }
-      }
-    }
-  }
+  sums.store(p, w, row0, lane, lse);
 }
 
+// ------------------------------------------------------------------------------ tile_kernel
+
+// One buffer of unpacked tokens in LDS: operands lane by lane, scales as fp32.
+template <class S, int NT>
+struct Unpacked {
+  uint4 k[NT][S::NB][64];
+  uint4 v[NT / 2][S::NB][2][64];
+  float4_t ks[NT][S::NG][4], vs[NT][S::NG][4];   // [tile][group][quad]
+  float vmax[2 * NT];                            // of each tile's values, by wave
+  int there[NT];
+};
+
+template <int KIND, int D, int GROUP, bool BF16, int RT>
+__global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
+  using S = Shape<KIND, D, GROUP, BF16>;
+  using C = Codes<KIND>;
+  constexpr int NT = tile_tiles(D), STEP = 16 * NT, TASKS = NT / 2;   // tiles of keys and of values, over four waves
+  using U = Unpacked<S, NT>;
+  extern __shared__ uint4 space[];
+  U* const buf = (U*)space;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+  const Span w = span_of(p, 4 * RT * 16);
+  const int row0 = (w.rb * 4 + wave) * (RT * 16);
+  const CacheRecord rec = cache_record(D, GROUP, 1 << p.page_shift, S::BITS);
+
+  uint32_t magic = 0x64006400u;
+  asm("" : "+v"(magic));
+  Raw<S::LB> raw[TASKS];
+  Scales<S::NG> sc[TASKS];
+  bool there[TASKS];
+  int pos[TASKS];
+  // task k of a wave: tile id % NT of keys (id < NT) or values, id = wave + 4 k
+  auto fetch = [&](int s0) {
+#pragma unroll
+    for (int k = 0; k < TASKS; ++k) {
+      const int id = wave + 4 * k, tile = id % NT;
+      pos[k] = s0 + 16 * tile;
+      const Place x = place_of(p, w, rec.total, pos[k]);
+      there[k] = x.there;
+      const uint8_t* scale;
+      if (id < NT) {
+        raw[k] = load_raw<S::LB, 64>(x.at + x.off * (D * S::BITS / 8), lane);
+        scale = x.at + rec.codes;
+      } else {
+        const uint8_t* v = x.at + rec.codes + rec.scales;
+        raw[k] = load_raw<S::LB, 16>(v + (x.off / 4 + g) * (D * S::BITS / 2), n);
+        scale = v + rec.codes;
+      }
+      sc[k] = load_scales<S::NG>(scale + (x.off / 4 + g) * (S::NG * 8));
+    }
+  };
+  auto unpack = [&](U& to) {
+#pragma unroll
+    for (int k = 0; k < TASKS; ++k) {
+      const int id = wave + 4 * k, tile = id % NT;
+      const bool keys = id < NT;
+      if (keys) {
+#pragma unroll
+        for (int B = 0; B < S::NB; ++B) to.k[tile][B][lane] = __builtin_bit_cast(uint4, C::key(raw[k].w, B, magic));
+        if (lane == 0) to.there[tile] = there[k];
+      } else {
+        if (pos[k] + 16 > w.end || !there[k]) drop_old<KIND>(raw[k], sc[k], held_bytes(w, pos[k] + 4 * g, there[k]));
+#pragma unroll
+        for (int B = 0; B < S::NB; ++B) {
+          uint2 f[2];
+          C::value(raw[k].w, B, magic, f);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ((uint2*)&to.v[tile >> 1][B][e][lane])[tile & 1] = f[e];
+        }
+        ushort2_t top = us2(sc[k].w[0][0]);
+#pragma unroll
+        for (int G = 0; G < S::NG; ++G)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) top = __builtin_elementwise_max(top, us2(sc[k].w[G][i]));
+        const float vmax = rows_max(__uint_as_float((uint32_t)max(top[0], top[1]) << 16));
+        if (lane == 0) to.vmax[tile] = vmax;
+      }
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G)
+        if (n == G)
+          (keys ? to.ks : to.vs)[tile][G][g] = float4_t{sc[k].get(G, 0), sc[k].get(G, 1), sc[k].get(G, 2), sc[k].get(G, 3)};
+    }
+  };
+
+  if (w.lo < w.hi) fetch(w.lo);
+  Rows<S, RT> rows;
+  rows.load(p, w, row0, lane);
+  Sums<S, RT> sums;
+  sums.clear();
+  if (w.lo < w.hi) {
+    unpack(buf[0]);
+    if (w.lo + STEP < w.hi) fetch(w.lo + STEP);
+  }
+  __syncthreads();
+
+  int at = 0;
+  for (int s0 = w.lo; s0 < w.hi; s0 += STEP, at ^= 1) {
+    U& u = buf[at];
+    // ---- scores over cs
+    float s[RT][4 * NT];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G) {
+        float4_t a[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) a[t] = float4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < S::BPG; ++j) {
+          const int B = G * S::BPG + j;
+          const half8_t kf = __builtin_bit_cast(half8_t, u.k[k][B][lane]);
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int c = 0; c < S::PIECES; ++c) a[t] = mfma(kf, rows.q[c][t][B], a[t]);
+        }
+        const float4_t ks = u.ks[k][G][g];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) s[t][4 * k + i] = G == 0 ? a[t][i] * ks[i] : fmaf(a[t][i], ks[i], s[t][4 * k + i]);
+      }
+    }
+    // ---- the next step's tokens into the other buffer (its readers passed the last barrier)
+    if (s0 + STEP < w.hi) {
+      unpack(buf[at ^ 1]);
+      if (s0 + 2 * STEP < w.hi) fetch(s0 + 2 * STEP);
+    }
+    bool all = true;
+    float vmax = u.vmax[0];
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      all = all && u.there[k];
+      vmax = fmaxf(vmax, u.vmax[k]);
+    }
+    if (s0 + STEP > w.ctx || !all) {
+#pragma unroll
+      for (int k = 0; k < NT; ++k) mask_scores<S>(s, 4 * k, p, w, rows, s0 + 16 * k + 4 * g, u.there[k]);
+    }
+    sums.rescale(s, rows.cs, vmax);
+    sums.weigh(s, rows.cs);
+
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int pr = 0; pr < NT / 2; ++pr)
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G) {
+        float4_t scale[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) scale[k] = u.vs[2 * pr + k][G][g] * sums.vinv;
+        half8_t pf[S::PIECES][RT];
+        weight_operands<S, KIND>(s, 8 * pr, scale, pf);
+#pragma unroll
+        for (int jb = 0; jb < S::BPG; ++jb) {
+          const int B = G * S::BPG + jb;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const half8_t vf = __builtin_bit_cast(half8_t, u.v[pr][B][e][lane]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+              for (int c = 0; c < S::PIECES; ++c) sums.acc[t][2 * B + e] = mfma(vf, pf[c][t], sums.acc[t][2 * B + e]);
+          }
+        }
+      }
+    __syncthreads();
+  }
+  float lse[RT];
+  sums.finish(rows.tok, lse);
+  sums.store(p, w, row0, lane, lse);
+}
+
+// ------------------------------------------------------------------------------------ launch
+
 template <int KIND, int D, int GROUP, bool BF16, int RT, int NW>
-hipError_t launch_shape(const AttnParams& p, hipStream_t s) {
-  const uint32_t grid = (uint32_t)((int64_t)p.nsplit * p.row_blocks * p.Hkv * p.B);
-  const size_t lds = (size_t)(NW - p.row_waves) * RT * (D / 4 + 1) * 64 * sizeof(float);
-  attn_kernel<KIND, D, GROUP, BF16, RT, NW><<<grid, NW * 64, lds, s>>>(p);
+hipError_t launch_stream(const AttnParams& p, uint32_t grid, hipStream_t s) {
+  const size_t lds = (size_t)(NW - 1) * RT * (D / 4 + 1) * 64 * sizeof(float);
+  stream_kernel<KIND, D, GROUP, BF16, RT, NW><<<grid, NW * 64, lds, s>>>(p);
+  return hipGetLastError();
+}
+
+template <int KIND, int D, int GROUP, bool BF16, int RT>
+hipError_t launch_tile(const AttnParams& p, uint32_t grid, hipStream_t s) {
+  using S = Shape<KIND, D, GROUP, BF16>;
+  tile_kernel<KIND, D, GROUP, BF16, RT><<<grid, 256, 2 * sizeof(Unpacked<S, tile_tiles(D)>), s>>>(p);
   return hipGetLastError();
 }
 
 template <int KIND, int D, int GROUP, bool BF16>
 hipError_t launch_by_plan(const AttnParams& p, const AttnPlan& a, hipStream_t s) {
+  const uint32_t grid = (uint32_t)((int64_t)p.nsplit * p.row_blocks * p.Hkv * p.B);
+  if (a.tiled) {
+    if constexpr (D <= 128)
+      if (a.row_tiles == 2) return launch_tile<KIND, D, GROUP, BF16, 2>(p, grid, s);
+    return launch_tile<KIND, D, GROUP, BF16, 1>(p, grid, s);
+  }
   if constexpr (D <= 128)
-    if (a.row_tiles == 2) return launch_shape<KIND, D, GROUP, BF16, 2, 4>(p, s);
-  if (a.waves == 8) return launch_shape<KIND, D, GROUP, BF16, 1, 8>(p, s);
-  return launch_shape<KIND, D, GROUP, BF16, 1, 4>(p, s);
+    if (a.row_tiles == 2) return launch_stream<KIND, D, GROUP, BF16, 2, 4>(p, grid, s);
+  if (a.waves == 8) return launch_stream<KIND, D, GROUP, BF16, 1, 8>(p, grid, s);
+  return launch_stream<KIND, D, GROUP, BF16, 1, 4>(p, grid, s);
 }
 
 template <int KIND, int D>

@@ -75,17 +75,18 @@ namespace pace {
 AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   AttnPlan a;
   const int64_t R = (int64_t)T * (c.Hq / c.Hkv);
-  a.row_tiles = c.d <= 128 && R > 16 ? 2 : 1;
-  const int tiles = ceil_div(R, 16 * a.row_tiles);
-  a.row_waves = tiles >= 3 ? 4 : tiles;
-  a.row_blocks = ceil_div(tiles, a.row_waves);
+  a.tiled = R > (c.d <= 128 ? 32 : 16);
+  a.row_tiles = c.d <= 128 && R > (a.tiled ? 64 : 16) ? 2 : 1;
+  a.waves = 4;
+  a.rows = 16 * a.row_tiles * (a.tiled ? a.waves : 1);
+  a.row_blocks = ceil_div(R, a.rows);
   const int64_t base = (int64_t)a.row_blocks * c.B * c.Hkv;
-  a.waves = a.row_tiles == 1 && a.row_waves == 1 && base <= 256 && max_len <= 1024 ? 8 : 4;
-  const int step = 32 * (a.waves / a.row_waves);     // tokens all waves of a workgroup take at once
-  const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, 2048 / base);
-  const int most = ceil_div(max_len, 2 * step);
+  if (!a.tiled && a.row_tiles == 1 && base <= 256 && max_len <= 1024) a.waves = 8;
+  a.step = 16 * (a.tiled ? tile_tiles(c.d) : stream_tiles(cache_bits(c.kind), c.d, a.row_tiles) * a.waves);
+  const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, 768 / base);
+  const int most = ceil_div(max_len, 2 * a.step);
   const int n = (int)std::min<int64_t>(std::min<int64_t>(want, most), kMaxPieces);
-  a.chunk = ceil_div(ceil_div(max_len, n), step) * step;
+  a.chunk = ceil_div(ceil_div(max_len, n), a.step) * a.step;
   a.nsplit = ceil_div(max_len, a.chunk);
   return a;
 }
@@ -302,7 +303,7 @@ pace_status pace_cache_attention(const pace_cache_cfg* cfg, const void* cache,
   p.num_pages = cfg->num_pages;
   p.max_pages = cfg->max_pages;
   p.nsplit = plan.nsplit; p.chunk = plan.chunk;
-  p.row_waves = plan.row_waves; p.row_blocks = plan.row_blocks;
+  p.row_blocks = plan.row_blocks;
   if (need) {
     p.part_o = (float*)workspace;
     p.part_lse = p.part_o + (size_t)plan.nsplit * cfg->B * cfg->Hkv * (size_t)p.R * cfg->d;

@@ -65,17 +65,27 @@ struct AttnParams {
   int32_t B, T, Hq, Hkv, gamma, R;   // R = T * gamma rows of one key/value head
   int32_t page_shift, num_pages, max_pages;
   int32_t nsplit, chunk;       // the context is cut into nsplit pieces of `chunk` tokens
-  int32_t row_waves, row_blocks;
+  int32_t row_blocks;
 };
 
 constexpr int kMaxPieces = 1024;   // of one context (the join keeps their weights in LDS)
 
+// 16-token tiles that a wave of stream_kernel takes at once: four where their codes still leave
+// registers for the next four (more bytes in flight, and the maximum's exchange paid half as
+// often), else two; and that a workgroup of tile_kernel unpacks at once.
+__host__ __device__ constexpr int stream_tiles(int bits, int d, int row_tiles) {
+  return row_tiles == 1 && d * bits <= 512 ? 4 : 2;
+}
+__host__ __device__ constexpr int tile_tiles(int d) { return d <= 128 ? 4 : 2; }
+
 // How pace_cache_attention cuts its work (a function of host-known sizes only).
 struct AttnPlan {
+  bool tiled;           // tile_kernel (waves on different rows) or stream_kernel (on tokens)
   int32_t row_tiles;    // 16-row tiles a wave holds
   int32_t waves;        // of a workgroup: 4 or 8
-  int32_t row_waves;    // of them on different rows (the others on different tokens)
+  int32_t rows;         // of a workgroup
   int32_t row_blocks;   // workgroups over the rows
+  int32_t step;         // tokens a workgroup takes at once
   int32_t nsplit, chunk;
 };
 AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len);

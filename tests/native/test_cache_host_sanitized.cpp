@@ -67,11 +67,13 @@ int main() {
                                                 X, nullptr, need ? X : nullptr, need, nullptr);
     EXPECT(st == PACE_OK && launches == before + 1);
     // every row is in exactly one workgroup, every token in exactly one piece
-    const int64_t rows = (int64_t)at_plan.row_blocks * at_plan.row_waves * at_plan.row_tiles * 16;
-    EXPECT(rows >= at.R && rows - (int64_t)at_plan.row_waves * at_plan.row_tiles * 16 < at.R);
-    EXPECT(at_plan.row_waves == 1 || at_plan.row_waves == 2 || at_plan.row_waves == 4);
-    EXPECT(at_plan.waves == 4 || at_plan.waves == 8);
-    EXPECT(at.nsplit >= 1 && at.chunk % (32 * (at_plan.waves / at_plan.row_waves)) == 0);
+    EXPECT((int64_t)at_plan.row_blocks * at_plan.rows >= at.R && (int64_t)(at_plan.row_blocks - 1) * at_plan.rows < at.R);
+    EXPECT(at_plan.rows == 16 * at_plan.row_tiles * (at_plan.tiled ? 4 : 1) && at.row_blocks == at_plan.row_blocks);
+    EXPECT(at_plan.waves == 4 || (at_plan.waves == 8 && !at_plan.tiled && at_plan.row_tiles == 1));
+    EXPECT(at_plan.row_tiles == 1 || (at_plan.row_tiles == 2 && c.d <= 128));
+    EXPECT(at.nsplit >= 1 && at.nsplit <= kMaxPieces && at.chunk % at_plan.step == 0);
+    EXPECT(at_plan.step == 16 * (at_plan.tiled ? tile_tiles(c.d)
+                                               : stream_tiles(c.kind == PACE_CACHE_INT4 ? 4 : 8, c.d, at_plan.row_tiles) * at_plan.waves));
     EXPECT((int64_t)at.nsplit * at.chunk >= max_len && (int64_t)(at.nsplit - 1) * at.chunk < max_len);
     EXPECT((need != 0) == (at.nsplit > 1));
     if (need) {
