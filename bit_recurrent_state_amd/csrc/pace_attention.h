@@ -200,13 +200,21 @@ struct Span {
 };
 __device__ inline Span span_of(const AttnParams& p, int rows) {
   Span w;
-  int id = blockIdx.x;
-  w.split = id % p.nsplit;
-  id /= p.nsplit;
-  w.rb = id % p.row_blocks;
-  id /= p.row_blocks;
-  w.h = id % p.Hkv;
-  w.b = id / p.Hkv;
+  // Workgroups go round the eight XCDs in turn.  Blocks of rows that read the same tokens are put
+  // on one XCD, whose L2 then reads them once: of the groups (sequence, head, piece), the first
+  // multiple of eight in this way, the rest in order.
+  int id = blockIdx.x, group = id;
+  w.rb = 0;
+  if (p.row_blocks > 1) {
+    const int whole = (p.B * p.Hkv * p.nsplit) & ~7, main = whole * p.row_blocks;
+    const int local = id < main ? id >> 3 : id - main;
+    w.rb = local % p.row_blocks;
+    group = id < main ? (local / p.row_blocks) * 8 + (id & 7) : whole + local / p.row_blocks;
+  }
+  w.split = group % p.nsplit;
+  group /= p.nsplit;
+  w.h = group % p.Hkv;
+  w.b = group / p.Hkv;
   const int capacity = p.max_pages << p.page_shift;
   w.ctx = min(max(p.ctx_lens[w.b], 0), capacity);
   w.drafts = p.draft_lens ? min(max(p.draft_lens[w.b], 0), p.T) : p.T;
@@ -218,18 +226,33 @@ __device__ inline Span span_of(const AttnParams& p, int rows) {
   return w;
 }
 
+// The page ids of 64 entries of the table, one a lane: a lookup is a lane read, with no memory
+// access to wait for but once in 64 pages.
+struct PageIds {
+  const int32_t* table;   // of the sequence
+  int32_t ids, base;
+  __device__ void load(const AttnParams& p, int entry, int lane) {
+    base = entry;
+    ids = table[min(base + lane, p.max_pages - 1)];
+  }
+  __device__ int get(const AttnParams& p, int entry, int lane) {
+    if ((uint32_t)(entry - base) >= 64u) load(p, entry, lane);
+    return __builtin_amdgcn_readlane(ids, entry - base);
+  }
+};
+
 // A 16-token tile in memory; one past the end is replaced by the last (and masked).
 struct Place {
   const uint8_t* at;   // the record
   uint32_t off;        // its first token in the page
   bool there;          // its page is one of the pool
 };
-__device__ inline Place place_of(const AttnParams& p, const Span& w, uint32_t record, int pos) {
+__device__ inline Place place_of(const AttnParams& p, const Span& w, PageIds& pages, uint32_t record, int pos, int lane) {
   const int tile = min(pos, max(w.end - 1, 0)) & ~15;
-  const int pg = uniform(p.table[(int64_t)w.b * p.max_pages + (tile >> p.page_shift)]);
+  const int pg = pages.get(p, tile >> p.page_shift, lane);
   Place r;
   r.there = pg >= 0 && pg < p.num_pages;
-  r.at = p.cache + ((int64_t)(r.there ? pg : 0) * p.Hkv + w.h) * record;
+  r.at = p.cache + ((uint64_t)(r.there ? (uint32_t)pg : 0u) * (uint32_t)p.Hkv + (uint32_t)w.h) * record;
   r.off = (uint32_t)(tile & ((1 << p.page_shift) - 1));
   return r;
 }
@@ -509,13 +532,15 @@ __global__ __launch_bounds__(NW * 64) void stream_kernel(AttnParams p) {
 
   Raw<S::LB> kr[NT], vr[NT];
   Scales<S::NG> ks[NT], vs[NT];
+  PageIds pages;
+  pages.table = p.table + (int64_t)w.b * p.max_pages;
   struct Where {
     Place t[NT];
   };
   auto where = [&](int s0) {
     Where x;
 #pragma unroll
-    for (int u = 0; u < NT; ++u) x.t[u] = place_of(p, w, rec.total, s0 + 16 * u);
+    for (int u = 0; u < NT; ++u) x.t[u] = place_of(p, w, pages, rec.total, s0 + 16 * u, lane);
     return x;
   };
   // use == 0 (no further step): every lane asks for the tile's first bytes, one cache line
@@ -538,6 +563,7 @@ __global__ __launch_bounds__(NW * 64) void stream_kernel(AttnParams p) {
   constexpr int stride = NW * STEP;
   Where cur;
   if (first < w.hi) {
+    pages.load(p, first >> p.page_shift, lane);
     cur = where(first);
     load_keys(cur, -1);
     load_values(cur, -1);
@@ -690,12 +716,12 @@ struct Unpacked {
   uint4 k[NT][S::NB][64];
   uint4 v[NT / 2][S::NB][2][64];
   float4_t ks[NT][S::NG][4], vs[NT][S::NG][4];   // [tile][group][quad]
-  float vmax[2 * NT];                            // of each tile's values, by wave
-  int there[NT];
+  float vmax[4];                                 // largest value scale of each tile (NT of them)
+  int there[4];                                  // whether each tile's page is one of the pool
 };
 
 template <int KIND, int D, int GROUP, bool BF16, int RT>
-__global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(AttnParams p) {
   using S = Shape<KIND, D, GROUP, BF16>;
   using C = Codes<KIND>;
   constexpr int NT = tile_tiles(D), STEP = 16 * NT, TASKS = NT / 2;   // tiles of keys and of values, over four waves
@@ -711,39 +737,40 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
   asm("" : "+v"(magic));
   Raw<S::LB> raw[TASKS];
   Scales<S::NG> sc[TASKS];
-  bool there[TASKS];
-  int pos[TASKS];
-  // task k of a wave: tile id % NT of keys (id < NT) or values, id = wave + 4 k
+  bool there;
+  int pos;
+  PageIds pages;
+  pages.table = p.table + (int64_t)w.b * p.max_pages;
+  // task k of a wave: keys (id < NT) or values of tile id % NT, id = wave + 4 k; a wave's tasks
+  // are of one tile
+  const int tile = wave % NT;
   auto fetch = [&](int s0) {
+    pos = s0 + 16 * tile;
+    const Place x = place_of(p, w, pages, rec.total, pos, lane);
+    there = x.there;
 #pragma unroll
     for (int k = 0; k < TASKS; ++k) {
-      const int id = wave + 4 * k, tile = id % NT;
-      pos[k] = s0 + 16 * tile;
-      const Place x = place_of(p, w, rec.total, pos[k]);
-      there[k] = x.there;
-      const uint8_t* scale;
-      if (id < NT) {
+      const bool keys = TASKS == 2 ? k == 0 : wave < NT;
+      if (keys) {
         raw[k] = load_raw<S::LB, 64>(x.at + x.off * (D * S::BITS / 8), lane);
-        scale = x.at + rec.codes;
+        sc[k] = load_scales<S::NG>(x.at + rec.codes + (x.off / 4 + g) * (S::NG * 8));
       } else {
         const uint8_t* v = x.at + rec.codes + rec.scales;
         raw[k] = load_raw<S::LB, 16>(v + (x.off / 4 + g) * (D * S::BITS / 2), n);
-        scale = v + rec.codes;
+        sc[k] = load_scales<S::NG>(v + rec.codes + (x.off / 4 + g) * (S::NG * 8));
       }
-      sc[k] = load_scales<S::NG>(scale + (x.off / 4 + g) * (S::NG * 8));
     }
   };
   auto unpack = [&](U& to) {
 #pragma unroll
     for (int k = 0; k < TASKS; ++k) {
-      const int id = wave + 4 * k, tile = id % NT;
-      const bool keys = id < NT;
+      const bool keys = TASKS == 2 ? k == 0 : wave < NT;
       if (keys) {
 #pragma unroll
         for (int B = 0; B < S::NB; ++B) to.k[tile][B][lane] = __builtin_bit_cast(uint4, C::key(raw[k].w, B, magic));
-        if (lane == 0) to.there[tile] = there[k];
+        if (lane == 0) to.there[tile] = there;
       } else {
-        if (pos[k] + 16 > w.end || !there[k]) drop_old<KIND>(raw[k], sc[k], held_bytes(w, pos[k] + 4 * g, there[k]));
+        if (pos + 16 > w.end || !there) drop_old<KIND>(raw[k], sc[k], held_bytes(w, pos + 4 * g, there));
 #pragma unroll
         for (int B = 0; B < S::NB; ++B) {
           uint2 f[2];
@@ -766,7 +793,10 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
     }
   };
 
-  if (w.lo < w.hi) fetch(w.lo);
+  if (w.lo < w.hi) {
+    pages.load(p, w.lo >> p.page_shift, lane);
+    fetch(w.lo);
+  }
   Rows<S, RT> rows;
   rows.load(p, w, row0, lane);
   Sums<S, RT> sums;
@@ -780,29 +810,37 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
   int at = 0;
   for (int s0 = w.lo; s0 < w.hi; s0 += STEP, at ^= 1) {
     U& u = buf[at];
-    // ---- scores over cs
+    // ---- scores over cs; a tile's operands are asked for while the tile before is multiplied
     float s[RT][4 * NT];
+    half8_t kf[2][S::NB];
+    float4_t ks[2][S::NG];
+    auto read_keys = [&](int k) {
+#pragma unroll
+      for (int B = 0; B < S::NB; ++B) kf[k & 1][B] = __builtin_bit_cast(half8_t, u.k[k][B][lane]);
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G) ks[k & 1][G] = u.ks[k][G][g];
+    };
+    read_keys(0);
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
+      if (k + 1 < NT) read_keys(k + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int G = 0; G < S::NG; ++G) {
         float4_t a[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) a[t] = float4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < S::BPG; ++j) {
-          const int B = G * S::BPG + j;
-          const half8_t kf = __builtin_bit_cast(half8_t, u.k[k][B][lane]);
+        for (int j = 0; j < S::BPG; ++j)
 #pragma unroll
           for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int c = 0; c < S::PIECES; ++c) a[t] = mfma(kf, rows.q[c][t][B], a[t]);
-        }
-        const float4_t ks = u.ks[k][G][g];
+            for (int c = 0; c < S::PIECES; ++c) a[t] = mfma(kf[k & 1][G * S::BPG + j], rows.q[c][t][G * S::BPG + j], a[t]);
+        const float4_t sc = ks[k & 1][G];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int t = 0; t < RT; ++t) s[t][4 * k + i] = G == 0 ? a[t][i] * ks[i] : fmaf(a[t][i], ks[i], s[t][4 * k + i]);
+          for (int t = 0; t < RT; ++t) s[t][4 * k + i] = G == 0 ? a[t][i] * sc[i] : fmaf(a[t][i], sc[i], s[t][4 * k + i]);
       }
     }
     // ---- the next step's tokens into the other buffer (its readers passed the last barrier)
@@ -810,43 +848,50 @@ __global__ __launch_bounds__(256) void tile_kernel(AttnParams p) {
       unpack(buf[at ^ 1]);
       if (s0 + 2 * STEP < w.hi) fetch(s0 + 2 * STEP);
     }
-    bool all = true;
-    float vmax = u.vmax[0];
+    const float4_t vm = *(const float4_t*)u.vmax;
+    const int4 th = *(const int4*)u.there;
+    const int here[4] = {th.x, th.y, th.z, th.w};
+    float vmax = vm[0];
+    int all = here[0];
 #pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      all = all && u.there[k];
-      vmax = fmaxf(vmax, u.vmax[k]);
+    for (int k = 1; k < NT; ++k) {
+      vmax = fmaxf(vmax, vm[k]);
+      all &= here[k];
     }
-    if (s0 + STEP > w.ctx || !all) {
+    if (s0 + STEP > w.ctx || !uniform(all)) {
 #pragma unroll
-      for (int k = 0; k < NT; ++k) mask_scores<S>(s, 4 * k, p, w, rows, s0 + 16 * k + 4 * g, u.there[k]);
+      for (int k = 0; k < NT; ++k) mask_scores<S>(s, 4 * k, p, w, rows, s0 + 16 * k + 4 * g, here[k] != 0);
     }
+    // ---- O^T += V^T P^T, block by block of 32 channels, a block's operands asked for one ahead
+    constexpr int NV = NT / 2 * S::NB;
+    half8_t vf[2][2];
+    auto read_values = [&](int i) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) vf[i & 1][e] = __builtin_bit_cast(half8_t, u.v[i / S::NB][i % S::NB][e][lane]);
+    };
+    read_values(0);
+    __builtin_amdgcn_sched_barrier(0);
     sums.rescale(s, rows.cs, vmax);
     sums.weigh(s, rows.cs);
-
-    // ---- O^T += V^T P^T
+    half8_t pf[S::PIECES][RT];
 #pragma unroll
-    for (int pr = 0; pr < NT / 2; ++pr)
-#pragma unroll
-      for (int G = 0; G < S::NG; ++G) {
+    for (int i = 0; i < NV; ++i) {
+      const int pr = i / S::NB, B = i % S::NB;
+      if (i + 1 < NV) read_values(i + 1);
+      if (B % S::BPG == 0) {
         float4_t scale[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) scale[k] = u.vs[2 * pr + k][G][g] * sums.vinv;
-        half8_t pf[S::PIECES][RT];
+        for (int k = 0; k < 2; ++k) scale[k] = u.vs[2 * pr + k][B / S::BPG][g] * sums.vinv;
         weight_operands<S, KIND>(s, 8 * pr, scale, pf);
-#pragma unroll
-        for (int jb = 0; jb < S::BPG; ++jb) {
-          const int B = G * S::BPG + jb;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const half8_t vf = __builtin_bit_cast(half8_t, u.v[pr][B][e][lane]);
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-              for (int c = 0; c < S::PIECES; ++c) sums.acc[t][2 * B + e] = mfma(vf, pf[c][t], sums.acc[t][2 * B + e]);
-          }
-        }
       }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int c = 0; c < S::PIECES; ++c) sums.acc[t][2 * B + e] = mfma(vf[i & 1][e], pf[c][t], sums.acc[t][2 * B + e]);
+    }
     __syncthreads();
   }
   float lse[RT];
