@@ -7,9 +7,66 @@
 namespace pace {
 namespace {
 
-constexpr int kJoin = 256;   // threads of a joining workgroup
+constexpr int kJoin = 256;       // threads of a joining workgroup
+constexpr int kFewPieces = 16;
 
-// Joins the pieces of a row.  One workgroup a row: D / 4 threads hold its channels, four each, and
+// Four channels of a row and its lse to where the caller wants them.
+template <int D, bool BF16>
+__device__ inline void store_row(const AttnParams& p, int64_t row, int c, float4 acc, float top, float sum) {
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int r = (int)(row % p.R), i = r / p.gamma;
+  const int64_t bh = row / p.R, b = bh / p.Hkv, h = bh % p.Hkv;
+  const int64_t at = (b * p.T + i) * p.Hq + h * p.gamma + (r - i * p.gamma);
+  if (c == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
+  if constexpr (BF16) {
+    auto pack = [&](float x, float y) {
+      return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(x * inv)) |
+             (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(y * inv)) << 16;
+    };
+    *(uint2*)((uint16_t*)p.o + at * D + 4 * c) = make_uint2(pack(acc.x, acc.y), pack(acc.z, acc.w));
+  } else {
+    *(float4*)((float*)p.o + at * D + 4 * c) = float4{acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  }
+}
+
+// Few pieces, usually of many rows: D / 4 threads a row, four channels each, which walk the pieces
+// themselves.  (A workgroup a row took 38 us for the 32768 rows of 2 pieces of a 512-token chunk.)
+template <int D, bool BF16>
+__global__ __launch_bounds__(kJoin) void join_few_kernel(AttnParams p) {
+  constexpr int C = D / 4;
+  const int64_t rows = (int64_t)p.B * p.Hkv * p.R, row = (int64_t)blockIdx.x * (kJoin / C) + threadIdx.x / C;
+  const int c = threadIdx.x % C;
+  if (row >= rows) return;
+  float l[kFewPieces];
+  float4 o[4];
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int s = 0; s < kFewPieces; ++s) {
+    l[s] = s < p.nsplit ? p.part_lse[s * rows + row] : -INFINITY;
+    top = fmaxf(top, l[s]);
+  }
+  if (top == -INFINITY) top = 0.f;      // nothing seen (or NaN everywhere)
+  float4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s0 = 0; s0 < kFewPieces; s0 += 4) {
+    if (s0 >= p.nsplit) break;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)         // an empty piece wrote no output
+      o[k] = l[s0 + k] != -INFINITY ? *(const float4*)(p.part_o + ((s0 + k) * rows + row) * D + 4 * c) : float4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = __builtin_amdgcn_exp2f(l[s0 + k] - top);
+      sum += f;
+      acc.x = fmaf(f, o[k].x, acc.x);
+      acc.y = fmaf(f, o[k].y, acc.y);
+      acc.z = fmaf(f, o[k].z, acc.z);
+      acc.w = fmaf(f, o[k].w, acc.w);
+    }
+  }
+  store_row<D, BF16>(p, row, c, acc, top, sum);
+}
+
+// Many pieces.  One workgroup a row: D / 4 threads hold its channels, four each, and
 // the 256 / (D / 4) groups of them take every so many-th piece, so that many pieces' loads are
 // in flight at once (one wave walking the pieces one by one took over 1 us a piece).  Weights
 // first, once, in LDS; sums in a fixed order.
@@ -67,32 +124,23 @@ __global__ __launch_bounds__(kJoin) void join_kernel(AttnParams p) {
     acc.z += o.z;
     acc.w += o.w;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int r = (int)(row % p.R), i = r / p.gamma;
-  const int64_t bh = row / p.R, b = bh / p.Hkv, h = bh % p.Hkv;
-  const int64_t at = (b * p.T + i) * p.Hq + h * p.gamma + (r - i * p.gamma);
-  if (c == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
-  if constexpr (BF16) {
-    auto pack = [&](float x, float y) {
-      return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(x * inv)) |
-             (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(y * inv)) << 16;
-    };
-    *(uint2*)((uint16_t*)p.o + at * D + 4 * c) = make_uint2(pack(acc.x, acc.y), pack(acc.z, acc.w));
-  } else {
-    *(float4*)((float*)p.o + at * D + 4 * c) = float4{acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-  }
+  store_row<D, BF16>(p, row, c, acc, top, sum);
+}
+
+template <int D, bool BF16>
+hipError_t join_d(const AttnParams& p, hipStream_t s) {
+  const int64_t rows = (int64_t)p.B * p.Hkv * p.R;
+  constexpr int per = kJoin / (D / 4);
+  if (p.nsplit <= kFewPieces)
+    join_few_kernel<D, BF16><<<(uint32_t)((rows + per - 1) / per), kJoin, 0, s>>>(p);
+  else
+    join_kernel<D, BF16><<<(uint32_t)rows, kJoin, 0, s>>>(p);
+  return hipGetLastError();
 }
 
 template <bool BF16>
 hipError_t join(const AttnParams& p, int d, hipStream_t s) {
-  const uint32_t grid = (uint32_t)((int64_t)p.B * p.Hkv * p.R);
-  if (d == 64)
-    join_kernel<64, BF16><<<grid, kJoin, 0, s>>>(p);
-  else if (d == 128)
-    join_kernel<128, BF16><<<grid, kJoin, 0, s>>>(p);
-  else
-    join_kernel<256, BF16><<<grid, kJoin, 0, s>>>(p);
-  return hipGetLastError();
+  return d == 64 ? join_d<64, BF16>(p, s) : d == 128 ? join_d<128, BF16>(p, s) : join_d<256, BF16>(p, s);
 }
 
 }  // namespace
