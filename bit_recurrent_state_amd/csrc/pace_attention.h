@@ -524,7 +524,7 @@ template <int KIND, int D, int GROUP, bool BF16, int RT, int NW>
 __global__ __launch_bounds__(NW * 64) void stream_kernel(AttnParams p) {
   using S = Shape<KIND, D, GROUP, BF16>;
   using C = Codes<KIND>;
-  constexpr int NT = stream_tiles(S::BITS, D, RT), STEP = 16 * NT;
+  constexpr int NT = kStreamTiles, STEP = 16 * NT;
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
   const Span w = span_of(p, RT * 16);
@@ -722,19 +722,17 @@ struct Unpacked {
   int there[4];                                  // whether each tile's page is one of the pool
 };
 
-template <int KIND, int D, int GROUP, bool BF16, int RT, int NW>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(RT == 1 && NW == 8 ? 4 : 2, RT == 1 && NW == 8 ? 4 : 2)))
-void tile_kernel(AttnParams p) {
+template <int KIND, int D, int GROUP, bool BF16, int RT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(AttnParams p) {
   using S = Shape<KIND, D, GROUP, BF16>;
   using C = Codes<KIND>;
-  constexpr int NT = tile_tiles(D), STEP = 16 * NT;
-  constexpr int TASKS = 2 * NT > NW ? 2 * NT / NW : 1;   // tiles of keys and of values, over the waves
+  constexpr int NT = tile_tiles(D), STEP = 16 * NT, TASKS = NT / 2;   // tiles of keys and of values, over four waves
   using U = Unpacked<S, NT>;
   extern __shared__ uint4 space[];
   U* const buf = (U*)space;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-  const Span w = span_of(p, NW * RT * 16);
-  const int row0 = (w.rb * NW + wave) * (RT * 16);
+  const Span w = span_of(p, 4 * RT * 16);
+  const int row0 = (w.rb * 4 + wave) * (RT * 16);
   const CacheRecord rec = cache_record(D, GROUP, 1 << p.page_shift, S::BITS);
 
   uint32_t magic = 0x64006400u;
@@ -745,12 +743,10 @@ void tile_kernel(AttnParams p) {
   int pos;
   PageIds pages;
   pages.table = p.table + (int64_t)w.b * p.max_pages;
-  // task k of a wave: keys (id < NT) or values of tile id % NT, id = wave + NW k < 2 NT; a wave's
-  // tasks are of one tile
+  // task k of a wave: keys (id < NT) or values of tile id % NT, id = wave + 4 k; a wave's tasks
+  // are of one tile
   const int tile = wave % NT;
-  const bool works = 2 * NT >= NW || wave < 2 * NT;
   auto fetch = [&](int s0) {
-    if (!works) return;
     pos = s0 + 16 * tile;
     const int at = tile_at(w, pos);
     const Place x = place_of(p, w, rec.total, at, pages.get(p, at >> p.page_shift, lane));
@@ -769,7 +765,6 @@ void tile_kernel(AttnParams p) {
     }
   };
   auto unpack = [&](U& to) {
-    if (!works) return;
 #pragma unroll
     for (int k = 0; k < TASKS; ++k) {
       const bool keys = TASKS == 2 ? k == 0 : wave < NT;
@@ -916,10 +911,10 @@ hipError_t launch_stream(const AttnParams& p, uint32_t grid, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int KIND, int D, int GROUP, bool BF16, int RT, int NW>
+template <int KIND, int D, int GROUP, bool BF16, int RT>
 hipError_t launch_tile(const AttnParams& p, uint32_t grid, hipStream_t s) {
   using S = Shape<KIND, D, GROUP, BF16>;
-  tile_kernel<KIND, D, GROUP, BF16, RT, NW><<<grid, NW * 64, 2 * sizeof(Unpacked<S, tile_tiles(D)>), s>>>(p);
+  tile_kernel<KIND, D, GROUP, BF16, RT><<<grid, 256, 2 * sizeof(Unpacked<S, tile_tiles(D)>), s>>>(p);
   return hipGetLastError();
 }
 
@@ -928,9 +923,8 @@ hipError_t launch_by_plan(const AttnParams& p, const AttnPlan& a, hipStream_t s)
   const uint32_t grid = (uint32_t)((int64_t)p.nsplit * p.row_blocks * p.Hkv * p.B);
   if (a.tiled) {
     if constexpr (D <= 128)
-      if (a.row_tiles == 2) return a.waves == 8 ? launch_tile<KIND, D, GROUP, BF16, 2, 8>(p, grid, s) : launch_tile<KIND, D, GROUP, BF16, 2, 4>(p, grid, s);
-    if (a.waves == 8) return launch_tile<KIND, D, GROUP, BF16, 1, 8>(p, grid, s);
-    return launch_tile<KIND, D, GROUP, BF16, 1, 4>(p, grid, s);
+      if (a.row_tiles == 2) return launch_tile<KIND, D, GROUP, BF16, 2>(p, grid, s);
+    return launch_tile<KIND, D, GROUP, BF16, 1>(p, grid, s);
   }
   if constexpr (D <= 128)
     if (a.row_tiles == 2) return launch_stream<KIND, D, GROUP, BF16, 2, 4>(p, grid, s);

@@ -82,7 +82,7 @@ AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   a.row_blocks = ceil_div(R, a.rows);
   const int64_t base = (int64_t)a.row_blocks * c.B * c.Hkv;
   if (!a.tiled && a.row_tiles == 1 && base <= 256 && max_len <= 1024) a.waves = 8;
-  a.step = 16 * (a.tiled ? tile_tiles(c.d) : stream_tiles(cache_bits(c.kind), c.d, a.row_tiles) * a.waves);
+  a.step = 16 * (a.tiled ? tile_tiles(c.d) : kStreamTiles * a.waves);
   const int64_t want = a.waves == 8 && !a.tiled ? 1 : std::max<int64_t>(1, 768 / base);
   const int most = ceil_div(max_len, 2 * a.step);
   const int n = (int)std::min<int64_t>(std::min<int64_t>(want, most), kMaxPieces);

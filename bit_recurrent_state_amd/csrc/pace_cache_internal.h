@@ -70,12 +70,9 @@ struct AttnParams {
 
 constexpr int kMaxPieces = 1024;   // of one context (the join keeps their weights in LDS)
 
-// 16-token tiles that a wave of stream_kernel takes at once: four where their codes still leave
-// registers for the next four (more bytes in flight, and the maximum's exchange paid half as
-// often), else two; and that a workgroup of tile_kernel unpacks at once.
-__host__ __device__ constexpr int stream_tiles(int bits, int d, int row_tiles) {
-  return row_tiles == 1 && d * bits <= 512 ? 4 : 2;
-}
+// 16-token tiles that a wave of stream_kernel takes at once (four instead of two cost registers, so
+// waves, and gained nothing), and that a workgroup of tile_kernel unpacks at once.
+constexpr int kStreamTiles = 2;
 __host__ __device__ constexpr int tile_tiles(int d) { return d <= 128 ? 4 : 2; }
 
 // How pace_cache_attention cuts its work (a function of host-known sizes only).

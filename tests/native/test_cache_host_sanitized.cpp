@@ -72,8 +72,7 @@ int main() {
     EXPECT(at_plan.waves == 4 || (at_plan.waves == 8 && !at_plan.tiled && at_plan.row_tiles == 1));
     EXPECT(at_plan.row_tiles == 1 || (at_plan.row_tiles == 2 && c.d <= 128));
     EXPECT(at.nsplit >= 1 && at.nsplit <= kMaxPieces && at.chunk % at_plan.step == 0);
-    EXPECT(at_plan.step == 16 * (at_plan.tiled ? tile_tiles(c.d)
-                                               : stream_tiles(c.kind == PACE_CACHE_INT4 ? 4 : 8, c.d, at_plan.row_tiles) * at_plan.waves));
+    EXPECT(at_plan.step == 16 * (at_plan.tiled ? tile_tiles(c.d) : kStreamTiles * at_plan.waves));
     EXPECT((int64_t)at.nsplit * at.chunk >= max_len && (int64_t)(at.nsplit - 1) * at.chunk < max_len);
     EXPECT((need != 0) == (at.nsplit > 1));
     if (need) {
