@@ -722,8 +722,11 @@ struct Unpacked {
   int there[4];                                  // whether each tile's page is one of the pool
 };
 
+// LDS holds two workgroups a compute unit: registers for as many, and for one where the groups'
+// operands would spill.
 template <int KIND, int D, int GROUP, bool BF16, int RT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void tile_kernel(AttnParams p) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D / GROUP * D * (BF16 ? 1 : 2) >= 1024 ? 1 : 2, 2)))
+void tile_kernel(AttnParams p) {
   using S = Shape<KIND, D, GROUP, BF16>;
   using C = Codes<KIND>;
   constexpr int NT = tile_tiles(D), STEP = 16 * NT, TASKS = NT / 2;   // tiles of keys and of values, over four waves
@@ -813,39 +816,30 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   int at = 0;
   for (int s0 = w.lo; s0 < w.hi; s0 += STEP, at ^= 1) {
     U& u = buf[at];
-    // ---- scores over cs; a tile's operands are asked for while the tile before is multiplied
+    // ---- scores over cs
     float s[RT][4 * NT];
-    half8_t kf[2][S::NB];
-    float4_t ks[2][S::NG];
-    auto read_keys = [&](int k) {
 #pragma unroll
-      for (int B = 0; B < S::NB; ++B) kf[k & 1][B] = __builtin_bit_cast(half8_t, u.k[k][B][lane]);
-#pragma unroll
-      for (int G = 0; G < S::NG; ++G) ks[k & 1][G] = u.ks[k][G][g];
-    };
-    read_keys(0);
-#pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      if (k + 1 < NT) read_keys(k + 1);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int k = 0; k < NT; ++k)
 #pragma unroll
       for (int G = 0; G < S::NG; ++G) {
         float4_t a[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) a[t] = float4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < S::BPG; ++j)
+        for (int j = 0; j < S::BPG; ++j) {
+          const int B = G * S::BPG + j;
+          const half8_t kf = __builtin_bit_cast(half8_t, u.k[k][B][lane]);
 #pragma unroll
           for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int c = 0; c < S::PIECES; ++c) a[t] = mfma(kf[k & 1][G * S::BPG + j], rows.q[c][t][G * S::BPG + j], a[t]);
-        const float4_t sc = ks[k & 1][G];
+            for (int c = 0; c < S::PIECES; ++c) a[t] = mfma(kf, rows.q[c][t][B], a[t]);
+        }
+        const float4_t ks = u.ks[k][G][g];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int t = 0; t < RT; ++t) s[t][4 * k + i] = G == 0 ? a[t][i] * sc[i] : fmaf(a[t][i], sc[i], s[t][4 * k + i]);
+          for (int t = 0; t < RT; ++t) s[t][4 * k + i] = G == 0 ? a[t][i] * ks[i] : fmaf(a[t][i], ks[i], s[t][4 * k + i]);
       }
-    }
     // ---- the next step's tokens into the other buffer (its readers passed the last barrier)
     if (s0 + STEP < w.hi) {
       unpack(buf[at ^ 1]);
@@ -865,36 +859,32 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
       for (int k = 0; k < NT; ++k) mask_scores<S>(s, 4 * k, p, w, rows, s0 + 16 * k + 4 * g, here[k] != 0);
     }
-    // ---- O^T += V^T P^T, block by block of 32 channels, a block's operands asked for one ahead
-    constexpr int NV = NT / 2 * S::NB;
-    half8_t vf[2][2];
-    auto read_values = [&](int i) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) vf[i & 1][e] = __builtin_bit_cast(half8_t, u.v[i / S::NB][i % S::NB][e][lane]);
-    };
-    read_values(0);
-    __builtin_amdgcn_sched_barrier(0);
     sums.rescale(s, rows.cs, vmax);
     sums.weigh(s, rows.cs);
-    half8_t pf[S::PIECES][RT];
+
+    // ---- O^T += V^T P^T
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int pr = i / S::NB, B = i % S::NB;
-      if (i + 1 < NV) read_values(i + 1);
-      if (B % S::BPG == 0) {
+    for (int pr = 0; pr < NT / 2; ++pr)
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G) {
         float4_t scale[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) scale[k] = u.vs[2 * pr + k][B / S::BPG][g] * sums.vinv;
+        for (int k = 0; k < 2; ++k) scale[k] = u.vs[2 * pr + k][G][g] * sums.vinv;
+        half8_t pf[S::PIECES][RT];
         weight_operands<S, KIND>(s, 8 * pr, scale, pf);
+#pragma unroll
+        for (int jb = 0; jb < S::BPG; ++jb) {
+          const int B = G * S::BPG + jb;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const half8_t vf = __builtin_bit_cast(half8_t, u.v[pr][B][e][lane]);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+              for (int c = 0; c < S::PIECES; ++c) sums.acc[t][2 * B + e] = mfma(vf, pf[c][t], sums.acc[t][2 * B + e]);
+          }
+        }
       }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int c = 0; c < S::PIECES; ++c) sums.acc[t][2 * B + e] = mfma(vf[i & 1][e], pf[c][t], sums.acc[t][2 * B + e]);
-    }
     __syncthreads();
   }
   float lse[RT];
@@ -922,13 +912,14 @@ template <int KIND, int D, int GROUP, bool BF16>
 hipError_t launch_by_plan(const AttnParams& p, const AttnPlan& a, hipStream_t s) {
   const uint32_t grid = (uint32_t)((int64_t)p.nsplit * p.row_blocks * p.Hkv * p.B);
   if (a.tiled) {
-    if constexpr (D <= 128)
+    if constexpr (tile_pairs(D, GROUP, BF16))
       if (a.row_tiles == 2) return launch_tile<KIND, D, GROUP, BF16, 2>(p, grid, s);
     return launch_tile<KIND, D, GROUP, BF16, 1>(p, grid, s);
   }
   if constexpr (D <= 128)
     if (a.row_tiles == 2) return launch_stream<KIND, D, GROUP, BF16, 2, 4>(p, grid, s);
-  if (a.waves == 8) return launch_stream<KIND, D, GROUP, BF16, 1, 8>(p, grid, s);
+  if constexpr (D <= 128)
+    if (a.waves == 8) return launch_stream<KIND, D, GROUP, BF16, 1, 8>(p, grid, s);
   return launch_stream<KIND, D, GROUP, BF16, 1, 4>(p, grid, s);
 }
 
