@@ -11,6 +11,8 @@
 // Bound by memory: inputs read once, codes and scales written once, about 15 operations a value.
 #include <hip/hip_runtime.h>
 
+#include <utility>
+
 #include "pace_cache_internal.h"
 #include "pace_lanes.h"
 #include "pace_numerics.h"
@@ -61,6 +63,30 @@ __device__ inline float tame(float x) {
   const bool nan = (f32_bits(x) & 0x7FFFFFFFu) > 0x7F800000u;
   return nan ? 0.f : fminf(fmaxf(x, -0x1p127f), 0x1p127f);
 }
+constexpr uint32_t kTame = 0x7F000000u;   // the bits of 2^127: larger magnitudes need it
+
+// Magnitudes compare as their bit patterns, which orders NaN last: one operation a value.
+__device__ inline uint32_t magnitude(const Run<float, 2>& x) {
+  return max(f32_bits(x.v[0]) & 0x7FFFFFFFu, f32_bits(x.v[1]) & 0x7FFFFFFFu);
+}
+__device__ inline uint32_t magnitude(const Run<float, 8>& x) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, f32_bits(x.v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
+__device__ inline ushort2_t magnitudes(uint32_t x) { return __builtin_bit_cast(ushort2_t, x & 0x7FFF7FFFu); }
+__device__ inline uint32_t magnitude(const Run<uint16_t, 2>& x) {
+  const ushort2_t m = magnitudes(__builtin_bit_cast(uint32_t, x));
+  return (uint32_t)max(m[0], m[1]) << 16;
+}
+__device__ inline uint32_t magnitude(const Run<uint16_t, 8>& x) {
+  const uint4 w = __builtin_bit_cast(uint4, x);
+  const ushort2_t m = __builtin_elementwise_max(__builtin_elementwise_max(magnitudes(w.x), magnitudes(w.y)),
+                                                __builtin_elementwise_max(magnitudes(w.z), magnitudes(w.w)));
+  return (uint32_t)max(m[0], m[1]) << 16;
+}
 
 // Scale and reciprocal of a group from its largest magnitude.
 template <int KIND>
@@ -71,29 +97,27 @@ __device__ inline void scale_of(float m, float& s, float& r) {
   r = s > 0.f ? rcp_bf16(s) : 0.f;
 }
 
-// The stored field of x: x / s, correctly rounded (r is the correctly rounded reciprocal, the
-// residual exact), then to the nearest code.
-template <int KIND>
+// x / s, correctly rounded (r is the correctly rounded reciprocal, the residual exact).  At most
+// L in magnitude, since s >= max|x| / L.
 __device__ inline float quotient(float x, float s, float r) {
-  constexpr float L = levels<KIND>();
   const float a = x * r, e = fmaf(-a, s, x);
-  return fminf(fmaxf(fmaf(e, r, a), -L), L);
+  return fmaf(e, r, a);
 }
+
+// The stored field of an int quotient above kField: adding 1.5 2^23 + offset rounds to the nearest
+// integer, ties to even (the offset is even), and leaves it in the low mantissa bits.
+constexpr uint32_t kField = 0x4B400000u;
 template <int KIND>
-__device__ inline void fields_of(float x, float y, float s, float r, uint32_t& f, uint32_t& h) {
-  float a = quotient<KIND>(x, s, r), b = quotient<KIND>(y, s, r);
-  if constexpr (KIND == PACE_CACHE_FP8) {
-    // the correction above turns -0 into +0: e4m3 keeps the quotient's sign (a zero group is +0)
-    a = s > 0.f ? copysignf(a, x) : 0.f;
-    b = s > 0.f ? copysignf(b, y) : 0.f;
-    const uint32_t w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    f = w & 0xFFu;
-    h = (w >> 8) & 0xFFu;
-  } else {
-    constexpr int offset = KIND == PACE_CACHE_INT8 ? 128 : 8;
-    f = (uint32_t)((int)rintf(a) + offset);
-    h = (uint32_t)((int)rintf(b) + offset);
-  }
+__device__ inline uint32_t int_field(float x, float s, float r) {
+  return f32_bits(quotient(x, s, r) + (12582912.0f + (KIND == PACE_CACHE_INT8 ? 128.f : 8.f)));
+}
+// Two e4m3 bytes.  The quotient's correction turns -0 into +0: e4m3 keeps the quotient's sign.
+__device__ inline uint32_t fp8_pair(float x, float y, float s, float r) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(copysignf(quotient(x, s, r), x), copysignf(quotient(y, s, r), y), 0, false);
+}
+// Four bytes from the low bytes of four fields.
+__device__ inline uint32_t four_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u), 0x05040100u);
 }
 
 template <int KIND>
@@ -104,12 +128,39 @@ __device__ inline float value_of(uint32_t f) {
     return (float)((int)f - (KIND == PACE_CACHE_INT8 ? 128 : 8));
 }
 
-// Maximum over the 16 lanes of a row, in every lane of it.
-__device__ inline float row_max(float x) {
-  x = fmaxf(x, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x128, 0xF, 0xF, true)));   // rotated by 8
-  x = fmaxf(x, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x124, 0xF, 0xF, true)));
-  x = fmaxf(x, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x122, 0xF, 0xF, true)));
-  return fmaxf(x, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), 0x121, 0xF, 0xF, true)));
+// Lane exchanges inside a row of 16.
+template <int CTRL>
+__device__ inline uint32_t row_move(uint32_t x) { return __builtin_amdgcn_mov_dpp(x, CTRL, 0xF, 0xF, true); }
+constexpr int kMirror = 0x140, kHalfMirror = 0x141, kSwap2 = 0x4E, kSwap1 = 0xB1, kFromLane = 0x150;
+
+// One step of a reduce-scatter of N maxima over a row: lanes whose `upper` is set keep the upper half
+// of the array, their partners (CTRL) the lower; a single value is combined.
+template <int N, int CTRL>
+__device__ inline void scatter_step(uint32_t* v, bool upper) {
+  if constexpr (N == 1) {
+    v[0] = max(v[0], row_move<CTRL>(v[0]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const uint32_t keep = upper ? v[i + N / 2] : v[i], give = upper ? v[i] : v[i + N / 2];
+      v[i] = max(keep, row_move<CTRL>(give));
+    }
+  }
+}
+// f(0), f(1), .. with compile-time indexes (lane numbers have to be).
+template <int... K, typename F>
+__device__ inline void for_each(std::integer_sequence<int, K...>, F f) {
+  (f(std::integral_constant<int, K>{}), ...);
+}
+constexpr int half_of(int n) { return n > 1 ? n / 2 : 1; }
+// Maxima of N values over the 16 lanes of a row.  Lane m ends with value(s) m N / 16, or
+// m div (16 / N) where N < 16.
+template <int N>
+__device__ inline void scatter_max(uint32_t* v, int m) {
+  scatter_step<N, kMirror>(v, m & 8);
+  scatter_step<half_of(N), kHalfMirror>(v, m & 4);
+  scatter_step<half_of(half_of(N)), kSwap2>(v, m & 2);
+  scatter_step<half_of(half_of(half_of(N))), kSwap1>(v, m & 1);
 }
 
 // What a wave works on: sequence, head, and the token index of its first position.
@@ -189,30 +240,63 @@ __device__ inline void write_keys(const CacheIoParams& p, const Item& w, int lan
   for (int B = 0; B < S::NB; ++B) raw[B] = *(const Run<E, 8>*)(from + 32 * B);
   int pos, r;
   uint8_t* const at = record_of(p, w, t, rec.total, pos, r);
+  float x[S::NB][8];
+#pragma unroll
+  for (int B = 0; B < S::NB; ++B)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[B][i] = widen(raw[B].v[i]);
+  uint32_t top[S::NG], most = 0u;
+#pragma unroll
+  for (int G = 0; G < S::NG; ++G) {
+    top[G] = 0u;
+#pragma unroll
+    for (int j = 0; j < S::BPG; ++j) top[G] = max(top[G], magnitude(raw[G * S::BPG + j]));
+    most = max(most, top[G]);
+  }
+  if (__any(most > kTame)) {
+#pragma unroll
+    for (int G = 0; G < S::NG; ++G) {
+      top[G] = 0u;
+#pragma unroll
+      for (int j = 0; j < S::BPG; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float& y = x[G * S::BPG + j][i];
+          y = tame(y);
+          top[G] = max(top[G], f32_bits(y) & 0x7FFFFFFFu);
+        }
+    }
+  }
   uint32_t word[S::LB / 4];
   float s[S::NG];
 #pragma unroll
   for (int G = 0; G < S::NG; ++G) {
-    float m = 0.f, inv;
-#pragma unroll
-    for (int j = 0; j < S::BPG; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(tame(widen(raw[G * S::BPG + j].v[i]))));
-    scale_of<KIND>(rows_max(m), s[G], inv);
+    LanePair pr = pair16(top[G]);
+    pr = pair32(max(pr.lo, pr.hi));
+    float inv;
+    scale_of<KIND>(bits_f32(max(pr.lo, pr.hi)), s[G], inv);
 #pragma unroll
     for (int j = 0; j < S::BPG; ++j) {
       const int B = G * S::BPG + j;
-      uint32_t f[8];
+      if constexpr (KIND == PACE_CACHE_FP8) {
+        const uint32_t live = s[G] > 0.f ? 0xFFFFFFFFu : 0u;   // a zero group is +0
 #pragma unroll
-      for (int i = 0; i < 8; i += 2)
-        fields_of<KIND>(tame(widen(raw[B].v[i])), tame(widen(raw[B].v[i + 1])), s[G], inv, f[i], f[i + 1]);
-      if constexpr (KIND == PACE_CACHE_INT4) {
-        word[B] = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) word[B] |= f[i] << (4 * (i / 2 + 4 * (i & 1)));
+        for (int k = 0; k < 2; ++k)
+          word[2 * B + k] = live & ((fp8_pair(x[B][4 * k], x[B][4 * k + 1], s[G], inv) & 0xFFFFu) |
+                                    fp8_pair(x[B][4 * k + 2], x[B][4 * k + 3], s[G], inv) << 16);
       } else {
-        word[2 * B] = f[0] | f[1] << 8 | f[2] << 16 | f[3] << 24;
-        word[2 * B + 1] = f[4] | f[5] << 8 | f[6] << 16 | f[7] << 24;
+        uint32_t f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = int_field<KIND>(x[B][i], s[G], inv);
+        if constexpr (KIND == PACE_CACHE_INT4) {
+          // channel e in nibble e / 2 + 4 (e mod 2); kField's own bits, shifted and summed, come off
+          uint32_t w = f[0] - (kField + (kField << 4) + (kField << 8));
+          w += (f[2] << 4) + (f[4] << 8) + (f[6] << 12);
+          word[B] = w + (f[1] << 16) + (f[3] << 20) + (f[5] << 24) + (f[7] << 28);
+        } else {
+          word[2 * B] = four_bytes(f[0], f[1], f[2], f[3]);
+          word[2 * B + 1] = four_bytes(f[4], f[5], f[6], f[7]);
+        }
       }
     }
   }
@@ -241,35 +325,83 @@ __device__ inline void write_values(const CacheIoParams& p, const Item& w, int l
   }
   Quad q;
   q.find(p, w, t, rec.total);
-  // word 2 B + e (8 bits) or B (4 bits): one byte a token
-  uint32_t word[S::LB / 4];
-#pragma unroll
-  for (int i = 0; i < S::LB / 4; ++i) word[i] = 0u;
-  uint16_t s[4][S::NG];
+  // ---- the groups' maxima, j NG + G; each found by the lanes of the row together, its scale by
+  // the lane (or lanes) that end with it, from which every lane reads scale and reciprocal
+  constexpr int N = 4 * S::NG;
+  float x[4][S::NB][2];
+  uint32_t top[N], most = 0u;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int G = 0; G < S::NG; ++G) {
-      float mx = 0.f, sc, inv;
-#pragma unroll
-      for (int k = 0; k < S::BPG; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) mx = fmaxf(mx, fabsf(tame(widen(raw[j][G * S::BPG + k].v[e]))));
-      scale_of<KIND>(row_max(mx), sc, inv);
-      s[j][G] = (uint16_t)(f32_bits(sc) >> 16);
+      uint32_t& v = top[j * S::NG + G];
+      v = 0u;
 #pragma unroll
       for (int k = 0; k < S::BPG; ++k) {
         const int B = G * S::BPG + k;
-        uint32_t f, h;
-        fields_of<KIND>(tame(widen(raw[j][B].v[0])), tame(widen(raw[j][B].v[1])), sc, inv, f, h);
-        if constexpr (KIND == PACE_CACHE_INT4) {
-          word[B] |= (f | h << 4) << (8 * j);
-        } else {
-          word[2 * B] |= f << (8 * j);
-          word[2 * B + 1] |= h << (8 * j);
-        }
+        x[j][B][0] = widen(raw[j][B].v[0]);
+        x[j][B][1] = widen(raw[j][B].v[1]);
+        v = max(v, magnitude(raw[j][B]));
+      }
+      most = max(most, v);
+    }
+  if (__any(most > kTame)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G) {
+        uint32_t& v = top[j * S::NG + G];
+        v = 0u;
+#pragma unroll
+        for (int k = 0; k < S::BPG; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float& y = x[j][G * S::BPG + k][e];
+            y = tame(y);
+            v = max(v, f32_bits(y) & 0x7FFFFFFFu);
+          }
+      }
+  }
+  scatter_max<N>(top, m);
+  constexpr int PER = N > 16 ? N / 16 : 1;   // values a lane ends with
+  float sc[PER], inv[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) scale_of<KIND>(bits_f32(top[i]), sc[i], inv[i]);
+
+  // word 2 B + e (8 bits) or B (4 bits): one byte a token
+  uint32_t f[4][S::NB][2];
+  uint16_t s[4][S::NG];
+  for_each(std::make_integer_sequence<int, N>{}, [&](auto index) {   // group K = j NG + G
+    constexpr int K = decltype(index)::value;
+    constexpr int j = K / S::NG, G = K % S::NG, from = N >= 16 ? K * 16 / N : K * (16 / N), at = N > 16 ? K % PER : 0;
+    const float a = bits_f32(row_move<kFromLane + from>(f32_bits(sc[at]))), r = bits_f32(row_move<kFromLane + from>(f32_bits(inv[at])));
+    s[j][G] = (uint16_t)(f32_bits(a) >> 16);
+#pragma unroll
+    for (int k = 0; k < S::BPG; ++k) {
+      const int B = G * S::BPG + k;
+      if constexpr (KIND == PACE_CACHE_FP8) {
+        const uint32_t w = a > 0.f ? fp8_pair(x[j][B][0], x[j][B][1], a, r) : 0u;   // a zero group is +0
+        f[j][B][0] = w;
+        f[j][B][1] = w >> 8;
+      } else {
+        f[j][B][0] = int_field<KIND>(x[j][B][0], a, r);
+        f[j][B][1] = int_field<KIND>(x[j][B][1], a, r);
       }
     }
+  });
+  uint32_t word[S::LB / 4];
+#pragma unroll
+  for (int B = 0; B < S::NB; ++B) {
+    if constexpr (KIND == PACE_CACHE_INT4) {
+      uint32_t y[4];                         // both nibbles in the low byte
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = f[j][B][0] + (f[j][B][1] << 4);
+      word[B] = four_bytes(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) word[2 * B + e] = four_bytes(f[0][B][e], f[1][B][e], f[2][B][e], f[3][B][e]);
+    }
+  }
   const uint32_t codes_at = rec.codes + rec.scales, scales_at = codes_at + rec.codes;
   if (q.whole) {
 #pragma unroll
