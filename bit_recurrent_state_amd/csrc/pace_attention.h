@@ -13,13 +13,16 @@
 // The softmax keeps a running maximum that may lag by kLag octaves (weights up to
 // 2^(kLift + kLag), which fp16 holds), so accumulators are rescaled only when it is exceeded.
 //
-// Two kernels (the choice is attn_plan's, by sizes):
-//   stream_kernel, for up to 32 rows: every wave takes other tokens for all rows, straight from
-//     memory into registers; the waves' results are joined in LDS.  Bound by the cache's bytes.
-//   tile_kernel, for more rows: every wave takes other rows; the workgroup unpacks each tile of
-//     tokens once, into LDS in operand order, for all four waves.  Bound by the vector unit (about
-//     nine operations a score) beside the matrix unit.
-// Long contexts are cut over workgroups, joined by a second kernel (pace_attention.hip).
+// Work split: a wave holds one or two 16-row tiles and takes 32 cached tokens at a time, straight
+// from memory into registers, the next ones asked for while these are multiplied; the waves of a
+// workgroup take different tokens of the same rows and are joined in LDS at the end; long
+// contexts are also cut over workgroups, joined by a second kernel (pace_attention.hip); more rows
+// are more workgroups over the same tokens.  With few rows the cache's bytes bound it (8-bit codes at
+// the rate of a large copy; 4-bit ones at two thirds of it, where unpacking takes half of the vector
+// unit's time), with many rows the vector unit: nine operations a score and one a code beside
+// 256 matrix operations.  (A kernel that unpacked every token once a workgroup, into LDS, for waves
+// on different rows was 7% faster for a 512-token chunk of an int8 cache and 5 to 40% slower
+// everywhere else: its barriers and LDS waits cost more than the unpacking they saved.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -101,23 +104,25 @@ struct Codes {
     }
     return frag(w[0], w[1], w[2], w[3]);
   }
-  // channels 32 B + 2 n + {0, 1} of the lane's quad of one tile: half of an operand each
-  static __device__ void value(const uint32_t* v, int B, uint32_t magic, uint2 (&f)[2]) {
-    if constexpr (KIND == PACE_CACHE_INT4) {
-      two(v[B], magic, f[0].x, f[1].x);
-      two(v[B] >> 8, magic, f[0].y, f[1].y);
-    } else {
-      four(v[2 * B], f[0].x, f[0].y);
-      four(v[2 * B + 1], f[1].x, f[1].y);
-    }
-  }
   // channels 32 B + 2 n + {0, 1} of the lane's quads of two tiles
   static __device__ void values(const uint32_t* v0, const uint32_t* v1, int B, uint32_t magic, half8_t (&f)[2]) {
-    uint2 a[2], b[2];
-    value(v0, B, magic, a);
-    value(v1, B, magic, b);
-    f[0] = frag(a[0].x, a[0].y, b[0].x, b[0].y);
-    f[1] = frag(a[1].x, a[1].y, b[1].x, b[1].y);
+    if constexpr (KIND == PACE_CACHE_INT4) {
+      uint32_t l[4], h[4];
+      two(v0[B], magic, l[0], h[0]);
+      two(v0[B] >> 8, magic, l[1], h[1]);
+      two(v1[B], magic, l[2], h[2]);
+      two(v1[B] >> 8, magic, l[3], h[3]);
+      f[0] = frag(l[0], l[1], l[2], l[3]);
+      f[1] = frag(h[0], h[1], h[2], h[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t w[4];
+        four(v0[2 * B + e], w[0], w[1]);
+        four(v1[2 * B + e], w[2], w[3]);
+        f[e] = frag(w[0], w[1], w[2], w[3]);
+      }
+    }
   }
 };
 
@@ -225,23 +230,6 @@ __device__ inline Span span_of(const AttnParams& p, int rows) {
   w.hi = uniform(w.split == p.nsplit - 1 ? w.end : min(w.end, w.lo + p.chunk));
   return w;
 }
-
-// The page ids of 64 entries of the table, one a lane: a lookup is a lane read, with no memory
-// access to wait for but once in 64 pages.  For tile_kernel, whose lookups' waits stood before
-// its barrier (a 512-token chunk over 7680: 269 -> 236 us); stream_kernel asks for ids one step ahead
-// instead, which is cheaper there (a decode step: 86 against 95 us).
-struct PageIds {
-  const int32_t* table;   // of the sequence
-  int32_t ids, base;
-  __device__ void load(const AttnParams& p, int entry, int lane) {
-    base = entry;
-    ids = table[min(base + lane, p.max_pages - 1)];
-  }
-  __device__ int get(const AttnParams& p, int entry, int lane) {
-    if ((uint32_t)(entry - base) >= 64u) load(p, entry, lane);
-    return __builtin_amdgcn_readlane(ids, entry - base);
-  }
-};
 
 // A 16-token tile in memory; one past the end is replaced by the last (and masked).
 struct Place {
@@ -518,13 +506,13 @@ __device__ inline void weight_operands(const float (&s)[RT][N], int at, const fl
   }
 }
 
-// ---------------------------------------------------------------------------- stream_kernel
+// ------------------------------------------------------------------------------------ kernel
 
 template <int KIND, int D, int GROUP, bool BF16, int RT, int NW>
-__global__ __launch_bounds__(NW * 64) void stream_kernel(AttnParams p) {
+__global__ __launch_bounds__(NW * 64) void attn_kernel(AttnParams p) {
   using S = Shape<KIND, D, GROUP, BF16>;
   using C = Codes<KIND>;
-  constexpr int NT = kStreamTiles, STEP = 16 * NT;
+  constexpr int NT = kTiles, STEP = 16 * NT;
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
   const Span w = span_of(p, RT * 16);
@@ -710,217 +698,23 @@ __global__ __launch_bounds__(NW * 64) void stream_kernel(AttnParams p) {
   sums.store(p, w, row0, lane, lse);
 }
 
-// ------------------------------------------------------------------------------ tile_kernel
-
-// One buffer of unpacked tokens in LDS: operands lane by lane, scales as fp32.
-template <class S, int NT>
-struct Unpacked {
-  uint4 k[NT][S::NB][64];
-  uint4 v[NT / 2][S::NB][2][64];
-  float4_t ks[NT][S::NG][4], vs[NT][S::NG][4];   // [tile][group][quad]
-  float vmax[4];                                 // largest value scale of each tile (NT of them)
-  int there[4];                                  // whether each tile's page is one of the pool
-};
-
-// LDS holds two workgroups a compute unit: registers for as many, and for one where the groups'
-// operands would spill.
-template <int KIND, int D, int GROUP, bool BF16, int RT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D / GROUP * D * (BF16 ? 1 : 2) >= 1024 ? 1 : 2, 2)))
-void tile_kernel(AttnParams p) {
-  using S = Shape<KIND, D, GROUP, BF16>;
-  using C = Codes<KIND>;
-  constexpr int NT = tile_tiles(D), STEP = 16 * NT, TASKS = NT / 2;   // tiles of keys and of values, over four waves
-  using U = Unpacked<S, NT>;
-  extern __shared__ uint4 space[];
-  U* const buf = (U*)space;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
-  const Span w = span_of(p, 4 * RT * 16);
-  const int row0 = (w.rb * 4 + wave) * (RT * 16);
-  const CacheRecord rec = cache_record(D, GROUP, 1 << p.page_shift, S::BITS);
-
-  uint32_t magic = 0x64006400u;
-  asm("" : "+v"(magic));
-  Raw<S::LB> raw[TASKS];
-  Scales<S::NG> sc[TASKS];
-  bool there;
-  int pos;
-  PageIds pages;
-  pages.table = p.table + (int64_t)w.b * p.max_pages;
-  // task k of a wave: keys (id < NT) or values of tile id % NT, id = wave + 4 k; a wave's tasks
-  // are of one tile
-  const int tile = wave % NT;
-  auto fetch = [&](int s0) {
-    pos = s0 + 16 * tile;
-    const int at = tile_at(w, pos);
-    const Place x = place_of(p, w, rec.total, at, pages.get(p, at >> p.page_shift, lane));
-    there = x.there;
-#pragma unroll
-    for (int k = 0; k < TASKS; ++k) {
-      const bool keys = TASKS == 2 ? k == 0 : wave < NT;
-      if (keys) {
-        raw[k] = load_raw<S::LB, 64>(x.at + x.off * (D * S::BITS / 8), lane);
-        sc[k] = load_scales<S::NG>(x.at + rec.codes + (x.off / 4 + g) * (S::NG * 8));
-      } else {
-        const uint8_t* v = x.at + rec.codes + rec.scales;
-        raw[k] = load_raw<S::LB, 16>(v + (x.off / 4 + g) * (D * S::BITS / 2), n);
-        sc[k] = load_scales<S::NG>(v + rec.codes + (x.off / 4 + g) * (S::NG * 8));
-      }
-    }
-  };
-  auto unpack = [&](U& to) {
-#pragma unroll
-    for (int k = 0; k < TASKS; ++k) {
-      const bool keys = TASKS == 2 ? k == 0 : wave < NT;
-      if (keys) {
-#pragma unroll
-        for (int B = 0; B < S::NB; ++B) to.k[tile][B][lane] = __builtin_bit_cast(uint4, C::key(raw[k].w, B, magic));
-        if (lane == 0) to.there[tile] = there;
-      } else {
-        if (pos + 16 > w.end || !there) drop_old<KIND>(raw[k], sc[k], held_bytes(w, pos + 4 * g, there));
-#pragma unroll
-        for (int B = 0; B < S::NB; ++B) {
-          uint2 f[2];
-          C::value(raw[k].w, B, magic, f);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) ((uint2*)&to.v[tile >> 1][B][e][lane])[tile & 1] = f[e];
-        }
-        ushort2_t top = us2(sc[k].w[0][0]);
-#pragma unroll
-        for (int G = 0; G < S::NG; ++G)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) top = __builtin_elementwise_max(top, us2(sc[k].w[G][i]));
-        const float vmax = rows_max(__uint_as_float((uint32_t)max(top[0], top[1]) << 16));
-        if (lane == 0) to.vmax[tile] = vmax;
-      }
-#pragma unroll
-      for (int G = 0; G < S::NG; ++G)
-        if (n == G)
-          (keys ? to.ks : to.vs)[tile][G][g] = float4_t{sc[k].get(G, 0), sc[k].get(G, 1), sc[k].get(G, 2), sc[k].get(G, 3)};
-    }
-  };
-
-  if (w.lo < w.hi) {
-    pages.load(p, w.lo >> p.page_shift, lane);
-    fetch(w.lo);
-  }
-  Rows<S, RT> rows;
-  rows.load(p, w, row0, lane);
-  Sums<S, RT> sums;
-  sums.clear();
-  if (w.lo < w.hi) {
-    unpack(buf[0]);
-    if (w.lo + STEP < w.hi) fetch(w.lo + STEP);
-  }
-  __syncthreads();
-
-  int at = 0;
-  for (int s0 = w.lo; s0 < w.hi; s0 += STEP, at ^= 1) {
-    U& u = buf[at];
-    // ---- scores over cs
-    float s[RT][4 * NT];
-#pragma unroll
-    for (int k = 0; k < NT; ++k)
-#pragma unroll
-      for (int G = 0; G < S::NG; ++G) {
-        float4_t a[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) a[t] = float4_t{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < S::BPG; ++j) {
-          const int B = G * S::BPG + j;
-          const half8_t kf = __builtin_bit_cast(half8_t, u.k[k][B][lane]);
-#pragma unroll
-          for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int c = 0; c < S::PIECES; ++c) a[t] = mfma(kf, rows.q[c][t][B], a[t]);
-        }
-        const float4_t ks = u.ks[k][G][g];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int t = 0; t < RT; ++t) s[t][4 * k + i] = G == 0 ? a[t][i] * ks[i] : fmaf(a[t][i], ks[i], s[t][4 * k + i]);
-      }
-    // ---- the next step's tokens into the other buffer (its readers passed the last barrier)
-    if (s0 + STEP < w.hi) {
-      unpack(buf[at ^ 1]);
-      if (s0 + 2 * STEP < w.hi) fetch(s0 + 2 * STEP);
-    }
-    const float4_t vm = *(const float4_t*)u.vmax;
-    const int4 th = *(const int4*)u.there;
-    const int here[4] = {th.x, th.y, th.z, th.w};
-    float vmax = vm[0];
-    int all = here[0];
-#pragma unroll
-    for (int k = 1; k < NT; ++k) {
-      vmax = fmaxf(vmax, vm[k]);
-      all &= here[k];
-    }
-    if (s0 + STEP > w.ctx || !uniform(all)) {
-#pragma unroll
-      for (int k = 0; k < NT; ++k) mask_scores<S>(s, 4 * k, p, w, rows, s0 + 16 * k + 4 * g, here[k] != 0);
-    }
-    sums.rescale(s, rows.cs, vmax);
-    sums.weigh(s, rows.cs);
-
-    // ---- O^T += V^T P^T
-#pragma unroll
-    for (int pr = 0; pr < NT / 2; ++pr)
-#pragma unroll
-      for (int G = 0; G < S::NG; ++G) {
-        float4_t scale[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) scale[k] = u.vs[2 * pr + k][G][g] * sums.vinv;
-        half8_t pf[S::PIECES][RT];
-        weight_operands<S, KIND>(s, 8 * pr, scale, pf);
-#pragma unroll
-        for (int jb = 0; jb < S::BPG; ++jb) {
-          const int B = G * S::BPG + jb;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const half8_t vf = __builtin_bit_cast(half8_t, u.v[pr][B][e][lane]);
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-              for (int c = 0; c < S::PIECES; ++c) sums.acc[t][2 * B + e] = mfma(vf, pf[c][t], sums.acc[t][2 * B + e]);
-          }
-        }
-      }
-    __syncthreads();
-  }
-  float lse[RT];
-  sums.finish(rows.tok, lse);
-  sums.store(p, w, row0, lane, lse);
-}
-
 // ------------------------------------------------------------------------------------ launch
 
 template <int KIND, int D, int GROUP, bool BF16, int RT, int NW>
-hipError_t launch_stream(const AttnParams& p, uint32_t grid, hipStream_t s) {
+hipError_t launch_shape(const AttnParams& p, uint32_t grid, hipStream_t s) {
   const size_t lds = (size_t)(NW - 1) * RT * (D / 4 + 1) * 64 * sizeof(float);
-  stream_kernel<KIND, D, GROUP, BF16, RT, NW><<<grid, NW * 64, lds, s>>>(p);
-  return hipGetLastError();
-}
-
-template <int KIND, int D, int GROUP, bool BF16, int RT>
-hipError_t launch_tile(const AttnParams& p, uint32_t grid, hipStream_t s) {
-  using S = Shape<KIND, D, GROUP, BF16>;
-  tile_kernel<KIND, D, GROUP, BF16, RT><<<grid, 256, 2 * sizeof(Unpacked<S, tile_tiles(D)>), s>>>(p);
+  attn_kernel<KIND, D, GROUP, BF16, RT, NW><<<grid, NW * 64, lds, s>>>(p);
   return hipGetLastError();
 }
 
 template <int KIND, int D, int GROUP, bool BF16>
 hipError_t launch_by_plan(const AttnParams& p, const AttnPlan& a, hipStream_t s) {
   const uint32_t grid = (uint32_t)((int64_t)p.nsplit * p.row_blocks * p.Hkv * p.B);
-  if (a.tiled) {
-    if constexpr (tile_pairs(D, GROUP, BF16))
-      if (a.row_tiles == 2) return launch_tile<KIND, D, GROUP, BF16, 2>(p, grid, s);
-    return launch_tile<KIND, D, GROUP, BF16, 1>(p, grid, s);
+  if constexpr (D <= 128) {
+    if (a.row_tiles == 2) return launch_shape<KIND, D, GROUP, BF16, 2, 4>(p, grid, s);
+    if (a.waves == 8) return launch_shape<KIND, D, GROUP, BF16, 1, 8>(p, grid, s);
   }
-  if constexpr (D <= 128)
-    if (a.row_tiles == 2) return launch_stream<KIND, D, GROUP, BF16, 2, 4>(p, grid, s);
-  if constexpr (D <= 128)
-    if (a.waves == 8) return launch_stream<KIND, D, GROUP, BF16, 1, 8>(p, grid, s);
-  return launch_stream<KIND, D, GROUP, BF16, 1, 4>(p, grid, s);
+  return launch_shape<KIND, D, GROUP, BF16, 1, 4>(p, grid, s);
 }
 
 template <int KIND, int D>

@@ -75,23 +75,19 @@ namespace pace {
 AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   AttnPlan a;
   const int64_t R = (int64_t)T * (c.Hq / c.Hkv);
-  const bool bf16 = c.io_dtype == PACE_IO_BF16;
-  a.tiled = R > (c.d <= 128 ? 32 : 16);
-  const bool pairs = a.tiled ? R > 64 && tile_pairs(c.d, c.group, bf16) : R > 16;
-  a.row_tiles = pairs ? 2 : 1;
-  a.waves = 4;
-  a.rows = 16 * a.row_tiles * (a.tiled ? a.waves : 1);
-  a.row_blocks = ceil_div(R, a.rows);
+  // Two row tiles a wave unpack every code once for 32 rows (a 512-token chunk over 7680 tokens:
+  // 240 us, with one 310); d = 256 has no registers for them.
+  a.row_tiles = c.d <= 128 && R > 16 ? 2 : 1;
+  a.row_blocks = ceil_div(R, 16 * a.row_tiles);
   const int64_t base = (int64_t)a.row_blocks * c.B * c.Hkv;
   // A short context of few sequences: eight waves take it in one workgroup, and no second kernel
   // has to join pieces (one sequence, 513 tokens, 8 heads: 8.3 us against 9.7).
-  if (!a.tiled && a.row_tiles == 1 && c.d <= 128 && base <= 256 && max_len <= 1024) a.waves = 8;
-  a.step = 16 * (a.tiled ? tile_tiles(c.d) : kStreamTiles * a.waves);
-  // Otherwise pieces until the 256 compute units hold two (tile_kernel, 512 tokens over 7680: 224 us,
-  // with a round and a half of workgroups 253) or three workgroups each (streams; and trees, whose
-  // more and shorter pieces even out ragged contexts: 60 us against 65), none under two steps.
-  const int64_t fill = a.tiled && base >= 256 ? 512 : 768;
-  const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, fill / base);
+  a.waves = a.row_tiles == 1 && c.d <= 128 && base <= 256 && max_len <= 1024 ? 8 : 4;
+  a.step = 16 * kTiles * a.waves;
+  // Otherwise pieces until the 256 compute units hold three workgroups each, none under two steps.
+  // (Twice as many cost 2% of three contexts of 131072 tokens and 20% of 64 ragged ones: every
+  // workgroup waits for its first tokens, and its part is written and read once more.)
+  const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, 768 / base);
   const int most = ceil_div(max_len, 2 * a.step);
   const int n = (int)std::min<int64_t>(std::min<int64_t>(want, most), kMaxPieces);
   a.chunk = ceil_div(ceil_div(max_len, n), a.step) * a.step;

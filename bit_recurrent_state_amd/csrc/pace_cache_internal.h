@@ -70,23 +70,13 @@ struct AttnParams {
 
 constexpr int kMaxPieces = 1024;   // of one context (the join keeps their weights in LDS)
 
-// 16-token tiles that a wave of stream_kernel takes at once (four instead of two cost registers, so
-// waves, and gained nothing), and that a workgroup of tile_kernel unpacks at once.
-constexpr int kStreamTiles = 2;
-__host__ __device__ constexpr int tile_tiles(int d) { return d <= 128 ? 4 : 2; }
-// Whether a wave of tile_kernel may hold two 16-row tiles: where 256 registers take them without
-// spilling (16 sequences x 25 drafts over 4096 tokens, d = 128, int8: g = 128 90 us against 104 with
-// one tile a wave; g = 32 464 against 129).
-__host__ __device__ constexpr bool tile_pairs(int d, int group, bool bf16) {
-  return d == 64 || (d == 128 && (group == 128 || (group == 64 && bf16)));
-}
+// 16-token tiles that a wave takes at once.  (Four cost registers, so waves, and gained nothing.)
+constexpr int kTiles = 2;
 
 // How pace_cache_attention cuts its work (a function of host-known sizes only).
 struct AttnPlan {
-  bool tiled;           // tile_kernel (waves on different rows) or stream_kernel (on tokens)
-  int32_t row_tiles;    // 16-row tiles a wave holds
-  int32_t waves;        // of a workgroup: 4 or 8
-  int32_t rows;         // of a workgroup
+  int32_t row_tiles;    // 16-row tiles a wave, and so a workgroup, holds
+  int32_t waves;        // of a workgroup, on different tokens: 4 or 8
   int32_t row_blocks;   // workgroups over the rows
   int32_t step;         // tokens a workgroup takes at once
   int32_t nsplit, chunk;

@@ -67,12 +67,12 @@ int main() {
                                                 X, nullptr, need ? X : nullptr, need, nullptr);
     EXPECT(st == PACE_OK && launches == before + 1);
     // every row is in exactly one workgroup, every token in exactly one piece
-    EXPECT((int64_t)at_plan.row_blocks * at_plan.rows >= at.R && (int64_t)(at_plan.row_blocks - 1) * at_plan.rows < at.R);
-    EXPECT(at_plan.rows == 16 * at_plan.row_tiles * (at_plan.tiled ? 4 : 1) && at.row_blocks == at_plan.row_blocks);
-    EXPECT(at_plan.waves == 4 || (at_plan.waves == 8 && !at_plan.tiled && at_plan.row_tiles == 1));
+    const int64_t rows = 16 * at_plan.row_tiles;
+    EXPECT(at_plan.row_blocks * rows >= at.R && (at_plan.row_blocks - 1) * rows < at.R && at.row_blocks == at_plan.row_blocks);
     EXPECT(at_plan.row_tiles == 1 || (at_plan.row_tiles == 2 && c.d <= 128));
+    EXPECT(at_plan.waves == 4 || (at_plan.waves == 8 && at_plan.row_tiles == 1 && c.d <= 128));
+    EXPECT(at_plan.step == 16 * kTiles * at_plan.waves);
     EXPECT(at.nsplit >= 1 && at.nsplit <= kMaxPieces && at.chunk % at_plan.step == 0);
-    EXPECT(at_plan.step == 16 * (at_plan.tiled ? tile_tiles(c.d) : kStreamTiles * at_plan.waves));
     EXPECT((int64_t)at.nsplit * at.chunk >= max_len && (int64_t)(at.nsplit - 1) * at.chunk < max_len);
     EXPECT((need != 0) == (at.nsplit > 1));
     if (need) {
