@@ -13,6 +13,7 @@ from ._lib import (  # noqa: F401
 )
 from ._cache import (  # noqa: F401
     CACHE_EXPORTS, CacheConfig, RotaryConfig, cache_attention, cache_attention_workspace_bytes,
-    cache_layout, cache_read, cache_write, rotary, rotary_freqs, tree_bits,
+    cache_layout, cache_read, cache_write, prepare_cache_attention, prepare_cache_write, prepare_rotary,
+    rotary, rotary_freqs, tree_bits,
 )
 from .presets import bf16_periodic, pace4, pace48, tiny_ref  # noqa: F401

@@ -127,6 +127,23 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _call(fn, name, args):
+    st = fn(*args)
+    if st != PACE_OK:
+        raise PaceError(st, name)
+
+
+def _prepared(fn, name, args, keep):
+    """The same call again with no Python-side checks (graph capture, timing loops); the tensors
+    stay alive with the callable."""
+    def call():
+        st = fn(*args)
+        if st != PACE_OK:
+            raise PaceError(st, name)
+    call._keep = (keep, args)
+    return call
+
+
 def _rows(t, name, dtype, lead, H, d):
     """(address, token stride) of a tensor [*lead, H, d] whose tokens are evenly spaced."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -164,10 +181,7 @@ def rotary_freqs(rd: int, base: float = 10000.0, scaling: str = "none", factor: 
     return f, m.value
 
 
-def rotary(cfg: RotaryConfig, positions, freqs, q, k, q_out, k_out, magnitude: float = 1.0,
-           inverse: bool = False, stream=None):
-    """pace_rotary.  q, q_out [n, Hq, d] and k, k_out [n, Hk, d] (None where the config has no
-    heads of it; the output may be the input); positions int32 [n]; freqs fp64 [rd / 2]."""
+def _rotary_args(cfg, positions, freqs, q, k, q_out, k_out, magnitude, inverse, stream):
     n = positions.numel()
     io, lead, d = _io(cfg), (n,), cfg.d
     qp = qo = kp = ko = None
@@ -176,11 +190,24 @@ def rotary(cfg: RotaryConfig, positions, freqs, q, k, q_out, k_out, magnitude: f
         (qp, qs), (qo, qos) = _rows(q, "q", io, lead, cfg.Hq, d), _rows(q_out, "q_out", io, lead, cfg.Hq, d)
     if cfg.Hk:
         (kp, ks), (ko, kos) = _rows(k, "k", io, lead, cfg.Hk, d), _rows(k_out, "k_out", io, lead, cfg.Hk, d)
-    st = LIB.pace_rotary(ctypes.byref(cfg._c), n, _ptr(positions, "positions", torch.int32),
-                         _ptr(freqs, "freqs", torch.float64, cfg.rd // 2), magnitude, int(inverse),
-                         qp, qs, kp, ks, qo, qos, ko, kos, _stream(stream))
-    if st != PACE_OK:
-        raise PaceError(st, "pace_rotary")
+    return (ctypes.byref(cfg._c), n, _ptr(positions, "positions", torch.int32),
+            _ptr(freqs, "freqs", torch.float64, cfg.rd // 2), magnitude, int(inverse),
+            qp, qs, kp, ks, qo, qos, ko, kos, _stream(stream))
+
+
+def rotary(cfg: RotaryConfig, positions, freqs, q, k, q_out, k_out, magnitude: float = 1.0,
+           inverse: bool = False, stream=None):
+    """pace_rotary.  q, q_out [n, Hq, d] and k, k_out [n, Hk, d] (None where the config has no
+    heads of it; the output may be the input); positions int32 [n]; freqs fp64 [rd / 2]."""
+    _call(LIB.pace_rotary, "pace_rotary",
+          _rotary_args(cfg, positions, freqs, q, k, q_out, k_out, magnitude, inverse, stream))
+
+
+def prepare_rotary(cfg: RotaryConfig, positions, freqs, q, k, q_out, k_out, magnitude: float = 1.0,
+                   inverse: bool = False, stream=None):
+    """Pre-marshalled pace_rotary (see prepare_decode_step)."""
+    args = _rotary_args(cfg, positions, freqs, q, k, q_out, k_out, magnitude, inverse, stream)
+    return _prepared(LIB.pace_rotary, "pace_rotary", args, (cfg, positions, freqs, q, k, q_out, k_out))
 
 
 # ------------------------------------------------------------------------------ cache
@@ -192,27 +219,33 @@ def cache_layout(cfg: CacheConfig) -> dict:
     return {f: getattr(info, f) for f, _ in _CacheInfo._fields_}
 
 
-def _cache_io(fn, name, cfg, cache, page_table, positions, k, v, stream):
+def _cache_io_args(cfg, cache, page_table, positions, k, v, stream):
     if positions.dim() != 2 or positions.shape[0] != cfg.B:
         raise ValueError(f"positions has shape {tuple(positions.shape)}, expected ({cfg.B}, T)")
     T = positions.shape[1]
     io = _io(cfg)
     kp, ks = _rows(k, "k", io, (cfg.B, T), cfg.Hkv, cfg.d)
     vp, vs = _rows(v, "v", io, (cfg.B, T), cfg.Hkv, cfg.d)
-    _check(fn(ctypes.byref(cfg._c), _ptr(cache, "cache", torch.uint8, cfg._bytes),
-              _ptr(page_table, "page_table", torch.int32, cfg.B * cfg.max_pages),
-              _ptr(positions, "positions", torch.int32), T, kp, ks, vp, vs, _stream(stream)), name)
+    return (ctypes.byref(cfg._c), _ptr(cache, "cache", torch.uint8, cfg._bytes),
+            _ptr(page_table, "page_table", torch.int32, cfg.B * cfg.max_pages),
+            _ptr(positions, "positions", torch.int32), T, kp, ks, vp, vs, _stream(stream))
 
 
 def cache_write(cfg: CacheConfig, cache, page_table, positions, k, v, stream=None):
     """pace_cache_write.  cache uint8 [cache_bytes]; page_table int32 [B, max_pages]; positions
     int32 [B, T] (negative: skipped); k, v [B, T, Hkv, d]."""
-    _cache_io(LIB.pace_cache_write, "pace_cache_write", cfg, cache, page_table, positions, k, v, stream)
+    _call(LIB.pace_cache_write, "pace_cache_write", _cache_io_args(cfg, cache, page_table, positions, k, v, stream))
 
 
 def cache_read(cfg: CacheConfig, cache, page_table, positions, k, v, stream=None):
     """pace_cache_read into k, v [B, T, Hkv, d] (zeros where a position is skipped)."""
-    _cache_io(LIB.pace_cache_read, "pace_cache_read", cfg, cache, page_table, positions, k, v, stream)
+    _call(LIB.pace_cache_read, "pace_cache_read", _cache_io_args(cfg, cache, page_table, positions, k, v, stream))
+
+
+def prepare_cache_write(cfg: CacheConfig, cache, page_table, positions, k, v, stream=None):
+    """Pre-marshalled pace_cache_write (see prepare_decode_step)."""
+    args = _cache_io_args(cfg, cache, page_table, positions, k, v, stream)
+    return _prepared(LIB.pace_cache_write, "pace_cache_write", args, (cfg, cache, page_table, positions, k, v))
 
 
 # -------------------------------------------------------------------------- attention
@@ -270,5 +303,13 @@ def cache_attention(cfg: CacheConfig, cache, page_table, q, ctx_lens, o, lse=Non
     lse fp32 [B, T, Hq] or None; scale 1 / sqrt(d) by default; max_len (host, default the
     table's capacity) what the work is laid out for; workspace uint8 of
     cache_attention_workspace_bytes(cfg, T, max_len)."""
-    _check(LIB.pace_cache_attention(*_attention_args(cfg, cache, page_table, q, ctx_lens, o, lse, tree, draft_lens,
-                                                     scale, max_len, workspace, stream)), "pace_cache_attention")
+    _call(LIB.pace_cache_attention, "pace_cache_attention",
+          _attention_args(cfg, cache, page_table, q, ctx_lens, o, lse, tree, draft_lens, scale, max_len, workspace, stream))
+
+
+def prepare_cache_attention(cfg: CacheConfig, cache, page_table, q, ctx_lens, o, lse=None, tree=None, draft_lens=None,
+                            scale=None, max_len=None, workspace=None, stream=None):
+    """Pre-marshalled pace_cache_attention (see prepare_decode_step)."""
+    args = _attention_args(cfg, cache, page_table, q, ctx_lens, o, lse, tree, draft_lens, scale, max_len, workspace, stream)
+    return _prepared(LIB.pace_cache_attention, "pace_cache_attention", args,
+                     (cfg, cache, page_table, q, ctx_lens, o, lse, tree, draft_lens, workspace))

@@ -598,3 +598,35 @@ def test_attention_fp32_weights_keep_both_pieces_at_ties():
     its fp16 piece, and its second piece has to match the first as the matrix unit got it."""
     s = Scene(31, 24, 4, 4, 64, "fp8", 32, 16, [9] * 24, False)
     s.check(6, [3] * 24)
+
+
+def test_prepared_calls_equal_plain_ones():
+    pace = _pace()
+    s = Scene(41, 2, 2, 2, 64, "int8", 64, 16, [60, 33], True, max_pages=6)
+    n = pace.cache_attention_workspace_bytes(s.cfg, 2, 96)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    x = dev(rounded(s.rng.standard_normal((3, 2, 2, 4, 64)), True), torch.bfloat16)
+    q, k, v = x[0], x[1, :, :, :2].contiguous(), x[2, :, :, :2].contiguous()
+    ctx, pos = dev(np.array([60, 33], np.int32)), dev(np.array([[60, 61], [33, 34]], np.int32))
+    f = dev(pace.rotary_freqs(32)[0])
+    rot = pace.RotaryConfig(Hq=4, Hk=2, d=64, rd=32)
+    out = []
+    for prepared in (False, True):
+        cache, qr, kr, o = s.cache.clone(), torch.empty_like(q), torch.empty_like(k), torch.empty_like(q)
+        flat = lambda t: t.view(4, -1, 64)  # noqa: E731
+        a = (rot, pos.view(-1), f, flat(q), flat(k), flat(qr), flat(kr))
+        b = (s.cfg, cache, s.table, pos, kr, v)
+        c = (s.cfg, cache, s.table, qr, ctx, o)
+        if prepared:
+            calls = [pace.prepare_rotary(*a), pace.prepare_cache_write(*b),
+                     pace.prepare_cache_attention(*c, max_len=96, workspace=ws)]
+            for call in calls + calls:
+                call()
+        else:
+            pace.rotary(*a)
+            pace.cache_write(*b)
+            pace.cache_attention(*c, max_len=96, workspace=ws)
+        torch.cuda.synchronize()
+        out.append((cache, qr, kr, o))
+    for x, y in zip(*out):
+        assert torch.equal(x, y)
