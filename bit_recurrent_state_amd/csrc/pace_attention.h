@@ -17,12 +17,20 @@
 // from memory into registers, the next ones asked for while these are multiplied; the waves of a
 // workgroup take different tokens of the same rows and are joined in LDS at the end; long
 // contexts are also cut over workgroups, joined by a second kernel (pace_attention.hip); more rows
-// are more workgroups over the same tokens.  With few rows the cache's bytes bound it (8-bit codes at
-// the rate of a large copy; 4-bit ones at two thirds of it, where unpacking takes half of the vector
-// unit's time), with many rows the vector unit: nine operations a score and one a code beside
-// 256 matrix operations.  (A kernel that unpacked every token once a workgroup, into LDS, for waves
-// on different rows was 7% faster for a 512-token chunk of an int8 cache and 5 to 40% slower
-// everywhere else: its barriers and LDS waits cost more than the unpacking they saved.)
+// are more workgroups over the same tokens.
+//
+// What bounds it (d = 128, bf16 rows; "busy" from the issue counters over the kernel's cycles).
+// Few rows, 8-bit codes: memory.  3 tokens over 131072, int8: 154 us, 5.3 TB/s, a large copy's rate.
+// Few rows, 4-bit codes: unpacking and latency.  64 tokens over 512 to 8192, g = 64: 89 us, 3.2 TB/s;
+// vector unit 49% busy, waves wait a quarter of their time, 1.2 of them a SIMD on average since the
+// contexts differ.  Many rows: the vector unit.  512 tokens of 2 sequences over 7680, int8: 231 us, 577
+// TFLOP/s; vector unit 69% busy, matrix unit 26%; 20 vector operations a score, unpacking among them.
+// Trees between the two: 16 of 25 tokens over 256 to 4096, fp8: 57 us, 222 TFLOP/s, vector unit 44% busy,
+// 1.15 waves a SIMD.
+//
+// (A kernel that unpacked every token once a workgroup, into LDS, for waves on different rows was 2 to
+// 7% faster for that chunk in int8 and int4 with g >= 64 and in fp32, and slower elsewhere: 2% in
+// fp8, 6% with d = 64, 16% with g = 32, 17 and 27% for chunks of 128 and 64 tokens, 4% for the trees.)
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -75,18 +75,24 @@ namespace pace {
 AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   AttnPlan a;
   const int64_t R = (int64_t)T * (c.Hq / c.Hkv);
-  // Two row tiles a wave unpack every code once for 32 rows (a 512-token chunk over 7680 tokens:
-  // 240 us, with one 310); d = 256 has no registers for them.
-  a.row_tiles = c.d <= 128 && R > 16 ? 2 : 1;
+  // Two row tiles a wave unpack every code once for 32 rows (d = 128, int8: a 512-token chunk over
+  // 7680 tokens 231 us, with one tile 307).  Up to 32 rows that saves nothing and one tile leaves
+  // more waves (16 trees of 5 to 8 tokens over 4096: 25 to 31 us, with two tiles 28 to 34); from there
+  // to 100 rows either may be ahead by up to 25% in bf16, and one tile is in fp32 (25-token trees: 58 us
+  // against 69).  d = 256 has no registers for two.
+  a.row_tiles = c.d <= 128 && R > 32 ? 2 : 1;
   a.row_blocks = ceil_div(R, 16 * a.row_tiles);
   const int64_t base = (int64_t)a.row_blocks * c.B * c.Hkv;
-  // A short context of few sequences: eight waves take it in one workgroup, and no second kernel
-  // has to join pieces (one sequence, 513 tokens, 8 heads: 8.3 us against 9.7).
-  a.waves = a.row_tiles == 1 && c.d <= 128 && base <= 256 && max_len <= 1024 ? 8 : 4;
+  // Short contexts of few sequences.  Four waves take 256 tokens in one workgroup.  For some more, eight
+  // do, and no second kernel has to be launched to join pieces: one sequence of 300 to 760 tokens, 8
+  // heads, takes 8.4 to 9.8 us a call against 11.5.  (In a graph, where launches are cheap, 7.3 to 9.5 us
+  // against 8.2 to 8.9: faster to about 512 tokens, and to 1000 with 16 sequences.)
+  a.waves = a.row_tiles == 1 && c.d <= 128 && base <= 256 && max_len > 256 && max_len <= 768 ? 8 : 4;
   a.step = 16 * kTiles * a.waves;
   // Otherwise pieces until the 256 compute units hold three workgroups each, none under two steps.
-  // (Twice as many cost 2% of three contexts of 131072 tokens and 20% of 64 ragged ones: every
-  // workgroup waits for its first tokens, and its part is written and read once more.)
+  // (Twice as many cost 6% of three contexts of 131072 tokens and 15% of 16 trees of 25, and
+  // gained 2% of 64 ragged ones: every workgroup waits for its first tokens, and its part is written
+  // and read once more.)
   const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, 768 / base);
   const int most = ceil_div(max_len, 2 * a.step);
   const int n = (int)std::min<int64_t>(std::min<int64_t>(want, most), kMaxPieces);

@@ -3,7 +3,9 @@
 // One workgroup takes kTok tokens: its threads first form the kTok * rd / 2 cosines and
 // sines in LDS (the angle's turn count in fp64, its fraction in fp32), then walk the tokens'
 // heads in units of 8 channels, 16 bytes a lane.  Bound by memory: every element is read and
-// written once; the trigonometry is shared by all heads of a token.
+// written once; the trigonometry is shared by all heads of a token.  32768 tokens of 40 heads of 128,
+// bf16: 126 us, 5.3 TB/s, a large copy's rate.  1021 tokens of 20 heads of 256, fp32: 9.4 us, 4.4 TB/s.
+// 64 tokens: 3.1 us, of which an empty launch is half.
 #include <hip/hip_runtime.h>
 
 #include "pace_cache_internal.h"
