@@ -23,8 +23,8 @@
 // Few rows, 8-bit codes: memory.  3 tokens over 131072, int8: 154 us, 5.3 TB/s, a large copy's rate.
 // Few rows, 4-bit codes: unpacking and latency.  64 tokens over 512 to 8192, g = 64: 89 us, 3.2 TB/s;
 // vector unit 49% busy, waves wait a quarter of their time, 1.2 of them a SIMD on average since the
-// contexts differ.  Many rows: the vector unit.  512 tokens of 2 sequences over 7680, int8: 231 us, 577
-// TFLOP/s; vector unit 69% busy, matrix unit 26%; 20 vector operations a score, unpacking among them.
+// contexts differ.  Many rows: the vector unit.  512 tokens of 2 sequences over 7680, int8: 220 to 234 us, 569
+// to 606 TFLOP/s; vector unit 69% busy, matrix unit 26%; 20 vector operations a score, unpacking among them.
 // Trees between the two: 16 of 25 tokens over 256 to 4096, fp8: 57 us, 222 TFLOP/s, vector unit 44% busy,
 // 1.15 waves a SIMD.
 //

@@ -78,9 +78,11 @@ AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   // Two row tiles a wave unpack every code once for 32 rows (d = 128, int8: a 512-token chunk over
   // 7680 tokens 231 us, with one tile 307).  Up to 32 rows that saves nothing and one tile leaves
   // more waves (16 trees of 5 to 8 tokens over 4096: 25 to 31 us, with two tiles 28 to 34); from there
-  // to 100 rows either may be ahead by up to 25% in bf16, and one tile is in fp32 (25-token trees: 58 us
-  // against 69).  d = 256 has no registers for two.
-  a.row_tiles = c.d <= 128 && R > 32 ? 2 : 1;
+  // to 100 rows either may be ahead by up to 25%, evenly on average.  fp32 with d = 128 has twice the
+  // operands: there trees of 9 to 25 tokens, 36 to 100 rows, take 43 to 85 us with one tile and 51 to 87 with
+  // two (8% on average), trees of 48, 95 to 131 against 86 to 123.  d = 256 has no registers for two.
+  const int one_tile = c.io_dtype == PACE_IO_F32 && c.d == 128 ? 128 : 32;
+  a.row_tiles = c.d <= 128 && R > one_tile ? 2 : 1;
   a.row_blocks = ceil_div(R, 16 * a.row_tiles);
   const int64_t base = (int64_t)a.row_blocks * c.B * c.Hkv;
   // Short contexts of few sequences.  Four waves take 256 tokens in one workgroup.  For some more, eight

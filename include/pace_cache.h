@@ -184,7 +184,7 @@ pace_status pace_tree_bits(const int32_t* parents, int32_t T, uint32_t* bits);
  * (NULL if 0).
  * Errors: PACE_EINVAL for null pointers, T < 1, max_len < 1, a negative tree_stride, a
  * non-finite scale, a workspace that is too small, misalignment; PACE_EUNSUPPORTED for
- * T * Hq / Hkv over 2^24. */
+ * T * Hq / Hkv over 2^24, or more rows or workgroups in all than 2^31 - 1. */
 pace_status pace_cache_attention(const pace_cache_cfg* cfg, const void* cache,
                                  const int32_t* page_table, const void* q, int64_t q_stride,
                                  int32_t T, const int32_t* ctx_lens, const int32_t* draft_lens,

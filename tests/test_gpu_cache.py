@@ -630,3 +630,12 @@ def test_prepared_calls_equal_plain_ones():
         out.append((cache, qr, kr, o))
     for x, y in zip(*out):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("longest", [256, 257, 768, 769])
+@pytest.mark.parametrize("T,gamma,bf16", [(1, 4, True), (8, 4, True), (11, 3, True), (32, 4, False), (43, 3, False)])
+def test_attention_at_the_edges_of_the_split(T, gamma, bf16, longest):
+    """One row tile or two, four waves or eight, one piece or more: rows on both sides of each
+    bound, with several row blocks, a ragged context and a sequence without one."""
+    s = Scene(43, 3, 1, gamma, 128, "int8", 128, 16, [longest, 200, T], bf16)
+    s.check(T, [longest - T, 200 - T, 0], max_len=longest)
