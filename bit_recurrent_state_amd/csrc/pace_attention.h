@@ -50,6 +50,7 @@ typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
 constexpr float kLift = 7.f;     // weights are 2^kLift exp(s - m): fp16 stays normal down to 2^-21
 constexpr float kLag = 8.f;      // octaves the running maximum may lag behind
 constexpr float kFloor = -1e30f; // running maximum before any token
+constexpr float kFar = 0x1p20f;  // running maxima past this: scores are rounded before they are compared
 
 __device__ inline half2_t h2(uint32_t x) { return __builtin_bit_cast(half2_t, x); }
 __device__ inline uint32_t u2(half2_t x) { return __builtin_bit_cast(uint32_t, x); }
@@ -326,6 +327,7 @@ struct Sums {
   float4_t acc[RT][NJ];   // [t][2 B + e][i]: channel 32 B + 2 (4 g + i) + e of row n
   float m[RT], l[RT];     // running maximum (base 2, all lanes of a row agree), sum of this lane
   float vunit, vinv;      // the running power of two over the value scales, its inverse
+  bool far;               // some row's maximum is past kFar (all lanes agree)
 
   __device__ void clear() {
 #pragma unroll
@@ -336,6 +338,7 @@ struct Sums {
       l[t] = 0.f;
     }
     vunit = vinv = 0.f;
+    far = false;
   }
 
   // New maxima: s[t] holds scores over cs, vmax a bound of the step's value scales (all lanes).
@@ -361,11 +364,13 @@ struct Sums {
       vf = vunit * vinv;
       vunit = now;
     }
+    bool past = false;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const float now = fmaxf(m[t], mx[t]);
       const float f = __builtin_amdgcn_exp2f(m[t] - now);
       m[t] = now;
+      past |= now != kFloor && fabsf(now) > kFar;
       l[t] *= f;
       const float both = f * vf;
 #pragma unroll
@@ -373,20 +378,37 @@ struct Sums {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][j][i] *= both;
     }
+    far = __any(past);
   }
 
-  // Scores become weights.
+  // Scores become weights.  The maximum is a rounded score: up to kFar it is off by 2^-4 at most, and one
+  // fused step takes it from exact products.  Past that the difference would keep the maximum's rounding,
+  // which soon is more than its own distance to the row (and 2^32 is past any exponent), so that
+  // the products are rounded as the maximum was: the row's largest weighs 1 whatever its size.
   template <int N>
   __device__ void weigh(float (&s)[RT][N], const float (&cs)[RT]) {
+    if (far) {
+#pragma clang fp contract(off)
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const float base = m[t] - kLift;
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float z = s[t][i] * cs[t];
+          s[t][i] = z - (m[t] - kLift);
+        }
+    } else {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[t][i] = fmaf(s[t][i], cs[t], kLift - m[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], cs[t], -base));   // one rounding, of the difference
+        s[t][i] = __builtin_amdgcn_exp2f(s[t][i]);
         l[t] += s[t][i];
       }
-    }
   }
 
   // This wave's outputs o = acc / l and the base-2 logarithms of the sums.

@@ -1,0 +1,57 @@
+"""Attention where scores, keys or queries are far from 1, against the fp64 oracle.
+
+In these cases one token leads its row by far more than a score's error, so the softmax is
+that token's one-hot whatever the scores' last bits, which the tests check on the oracle's side first.
+What is left of the error is the leader's own weight: 2^-11 of the output (bf16: a weight is rounded to
+fp16) or 2^-21 (fp32: two fp16 pieces), half a bf16 step (2^-8) for bf16 outputs, and for lse
+(d + 16) 2^-24 + 2^-21 of sum |q k| scale (the fp32 product, two-piece queries, the base-2 units and back)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from cache_scene import Held, rounded  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+KINDS = [("int8", 128, 128), ("int4", 128, 32), ("fp8", 64, 64)]
+
+
+def one_hot(held, q, T=1, tokens=None, max_len=None, sequences=None):
+    """Checks rows that one token leads (of these sequences; the others only have to be finite)."""
+    s = held.d ** -0.5
+    wo, wl, w = held.wanted(q, T)
+    dz = np.zeros(q.shape[:-1])
+    sequences = list(range(held.B)) if sequences is None else sequences
+    for b in sequences:
+        for hq in range(held.cfg.Hq):
+            k = held.k[b, :, hq // held.gamma]
+            z_abs = (np.abs(q[b, :, hq].astype(np.float64)) @ np.abs(k).T * abs(s)).max(-1)
+            dz[b, :, hq] = ((held.d + 16) * 2.0 ** -24 + 2.0 ** -21) * z_abs
+            assert np.all(z_abs * 1.45 < 2.0 ** 128), "the case has to fit fp32"
+            z = np.where(held.visible(T), q[b, :, hq].astype(np.float64) @ k.T * s, -np.inf)
+            z = np.sort(z, axis=-1)
+            if z.shape[-1] > 1:
+                assert np.all(z[:, -1] - z[:, -2] > 4 * dz[b, :, hq] + 60), "the case has to be one-hot"
+    if tokens is not None:
+        assert np.all(w[sequences].argmax(-1) == tokens)
+    o, lse = held.attend(q, T, max_len=max_len)
+    assert np.all(np.isfinite(o)) and np.all(np.isfinite(lse))
+    E = 2.0 ** -8 * (1 + 2.0 ** -11) + 2.0 ** -11 if held.bf16 else 2.0 ** -21
+    for b in sequences:
+        assert np.all(np.abs(o[b] - wo[b]) <= E * np.abs(wo[b]) + 1e-30)
+        assert np.all(np.abs(lse[b] - wl[b]) <= dz[b] + 2.0 ** -21 * np.abs(wl[b]))
+
+
+@pytest.mark.parametrize("kind,d,g", KINDS)
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("size", [1e6, 1e9, 1e12, 1e20, 1e30])
+def test_scores_of_every_size(kind, d, g, bf16, size):
+    """Queries so long that scores reach 1e31: the leader's weight is exp(0) exactly, however coarse
+    fp32 is at its score."""
+    rng = np.random.default_rng(int(np.log10(size)) + d)
+    k, v = rng.standard_normal((2, 1, 300, 1, d))
+    held = Held(k, v, kind, g, bf16, gamma=3)
+    q = rounded(rng.standard_normal((1, 2, 3, d)) * size, bf16)
+    one_hot(held, q, T=2)
+    one_hot(held, q, T=2, max_len=4000)
