@@ -49,7 +49,7 @@ typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kLift = 7.f;     // weights are 2^kLift exp(s - m): fp16 stays normal down to 2^-21
 constexpr float kLag = 8.f;      // octaves the running maximum may lag behind
-constexpr float kFloor = -1e30f; // running maximum before any token
+constexpr float kFloor = -0x1.fffffep127f;   // running maximum before any token: no finite score is lower
 constexpr float kFar = 0x1p20f;  // running maxima past this: scores are rounded before they are compared
 
 __device__ inline half2_t h2(uint32_t x) { return __builtin_bit_cast(half2_t, x); }

@@ -55,3 +55,19 @@ def test_scores_of_every_size(kind, d, g, bf16, size):
     q = rounded(rng.standard_normal((1, 2, 3, d)) * size, bf16)
     one_hot(held, q, T=2)
     one_hot(held, q, T=2, max_len=4000)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("size", [1e28, 1e31, 1e34])
+def test_rows_whose_every_score_is_far_below_zero(bf16, size):
+    """A softmax does not depend on a common offset: rows whose scores are all near -1e30 or -1e35 are not
+    rows that see nothing."""
+    rng = np.random.default_rng(3)
+    d = 128
+    k, v = rng.standard_normal((2, 1, 40, 1, d))
+    k = np.abs(k) + 0.5
+    held = Held(k, v, "int8", 128, bf16)
+    q = rounded(-(np.abs(rng.standard_normal((1, 1, 1, d))) + 0.5) * size, bf16)
+    one_hot(held, q)
+    alone = Held(k[:, :1], v[:, :1], "int8", 128, bf16)
+    one_hot(alone, q)
