@@ -4,7 +4,7 @@
 // Mathematics.  The T * gamma rows of one key/value head (row r: token r div gamma, query head
 // r mod gamma) are the columns of S^T = K Q^T, so a matrix instruction v_mfma_f32_16x16x32_f16
 // takes 16 cached tokens against 16 rows.  Codes are exact in fp16: keys enter as they are
-// stored and their scales multiply the fp32 scores of a token.  Scores leave the instruction
+// stored and their scales (over 2^kDown, see Rows) multiply the fp32 scores of a token.  Scores leave the instruction
 // with four consecutive tokens of one row in a lane, and the product O^T = V^T P^T takes
 // its eight tokens a lane in any order, so with values stored by quads of tokens the weights go
 // straight from registers back into the matrix unit: no lane exchange but the row maximum.
@@ -50,9 +50,11 @@ typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
 constexpr float kLift = 7.f;     // weights are 2^kLift exp(s - m): fp16 stays normal down to 2^-21
 constexpr float kLag = 8.f;      // octaves the running maximum may lag behind
 constexpr float kFloor = -0x1.fffffep127f;   // running maximum before any token: no finite score is lower
+constexpr int kDown = 22;        // key scales enter the scores over 2^kDown (see Rows)
 constexpr float kFar = 0x1p20f;  // running maxima past this: scores are rounded before they are compared
 
 __device__ inline half2_t h2(uint32_t x) { return __builtin_bit_cast(half2_t, x); }
+__device__ inline ushort2_t us2(uint32_t x) { return __builtin_bit_cast(ushort2_t, x); }
 __device__ inline uint32_t u2(half2_t x) { return __builtin_bit_cast(uint32_t, x); }
 __device__ inline half8_t frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   const uint4 w = {a, b, c, d};
@@ -164,6 +166,15 @@ struct Scales {
     const uint32_t x = w[G][t >> 1];
     return __uint_as_float((t & 1) ? (x & 0xFFFF0000u) : (x << 16));
   }
+  // All of them over 2^n, `down` being n << 7 in both halves: exponent fields less n, 0 where that ends
+  // under the normal numbers.
+  __device__ void lower(uint32_t down) {
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[G][i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(us2(w[G][i]), us2(down)));
+  }
 };
 template <int NG>
 __device__ inline Scales<NG> load_scales(const uint8_t* base) {
@@ -181,7 +192,6 @@ __device__ inline Scales<NG> load_scales(const uint8_t* base) {
   return s;
 }
 
-__device__ inline ushort2_t us2(uint32_t x) { return __builtin_bit_cast(ushort2_t, x); }
 // Sum over a row's four lanes.
 __device__ inline float rows_sum(float x) {
   LanePair a = pair16(__float_as_uint(x));
@@ -262,10 +272,18 @@ struct Rows {
   float cs[RT];           // scores are cs * (K q)
   int tok[RT];            // the row's token, or -1
   const uint32_t* bits[RT];
+  // Scores are summed in units of cs, with queries of up to 2^14, 256 channels of them: a key of up to 2^127
+  // would leave fp32 there although the score itself does not.  So key scales are taken over 2^kDown,
+  // and cs makes up for it.  Scales under 2^(kDown - 126) then count as zero, which a query under 2^22
+  // does not notice (2^-64 of a score); where every query of the wave is larger, scores are large before
+  // sums are, and scales stay as they are.
+  uint32_t down;          // what Scales::lower takes
 
   __device__ void load(const AttnParams& p, const Span& w, int row0, int lane) {
     const int n = lane & 15, g = lane >> 4;
     constexpr int D = S::NB * 32;
+    float ups[RT];
+    bool small = false;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const int r = row0 + t * 16 + n, i = r / p.gamma;
@@ -301,8 +319,9 @@ struct Rows {
       int e = (int)(__float_as_uint(mx) >> 23) & 255;
       e = min(max(e, 14), 254);
       float up = __uint_as_float((uint32_t)min(140 - e + 127, 254) << 23);
+      ups[t] = up;
+      small |= mx > 0.f && e < 126 + 22;
       // the scale's sign goes into q, so that cs > 0 and masks can be -inf
-      cs[t] = p.scale_log2e == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2e) / up, 0x1p-126f);
       up = p.scale_log2e == 0.f ? 0.f : copysignf(up, p.scale_log2e);
 #pragma unroll
       for (int B = 0; B < S::NB; ++B) {
@@ -317,6 +336,12 @@ struct Rows {
         if constexpr (S::PIECES == 2) q[1][t][B] = frag(z[0], z[1], z[2], z[3]);
       }
     }
+    const bool lowered = __any(small);
+    down = lowered ? kDown * 0x00800080u : 0u;
+    const float scale = fabsf(p.scale_log2e) * (lowered ? (float)(1 << kDown) : 1.f);
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      cs[t] = p.scale_log2e == 0.f ? 1.f : fminf(fmaxf(scale / ups[t], 0x1p-126f), 0x1.fffffep127f);
   }
 };
 
@@ -604,6 +629,7 @@ __global__ __launch_bounds__(NW * 64) void attn_kernel(AttnParams p) {
     float s[RT][4 * NT];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
+      ks[u].lower(rows.down);
 #pragma unroll
       for (int G = 0; G < S::NG; ++G) {
         float4_t a[RT];

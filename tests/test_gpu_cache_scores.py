@@ -71,3 +71,47 @@ def test_rows_whose_every_score_is_far_below_zero(bf16, size):
     one_hot(held, q)
     alone = Held(k[:, :1], v[:, :1], "int8", 128, bf16)
     one_hot(alone, q)
+
+
+@pytest.mark.parametrize("kind,d,g", KINDS)
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("size", [1e30, 1e34, 1e36, np.inf])
+@pytest.mark.parametrize("channels", [1, 7])
+def test_keys_up_to_the_largest_that_a_cache_holds(kind, d, g, bf16, size, channels):
+    """A cache holds magnitudes up to 2^127 (infinities are stored so).  Scores over them are
+    finite for queries of ordinary size and smaller, so rows have to be as well."""
+    rng = np.random.default_rng(channels + d)
+    k, v = rng.standard_normal((2, 2, 77, 1, d))
+    for b, t, sign in ((0, 5, 1), (0, 40, -1), (1, 76, 1)):
+        k[b, t, 0, rng.permutation(d)[:channels]] = sign * size
+    held = Held(k, v, kind, g, bf16, gamma=2)
+    for scale in (1.0, 0.1, 1e-5):
+        q = rounded(np.abs(rng.standard_normal((2, 1, 2, d))) * scale, bf16)
+        one_hot(held, q, tokens=np.array([5, 76]).reshape(2, 1, 1))
+    # the other way round: one token far above, one or two far below the ordinary ones
+    q = rounded(-np.abs(rng.standard_normal((2, 1, 2, d))) * 0.3, bf16)
+    one_hot(held, q, sequences=[0], tokens=np.array([40]).reshape(1, 1, 1))
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_tiny_queries_over_large_keys_and_the_reverse(bf16):
+    """Scores of ordinary size from factors that are not: queries of 1e-30 over keys of 1e30, and queries
+    of 1e25 over keys of 1e-25.  Tolerance as for ordinary scores (tests/test_gpu_cache.py)."""
+    rng = np.random.default_rng(9)
+    d, L = 128, 200
+    for size in (1e30, 1e36, 1e-25):
+        k, v = rng.standard_normal((2, 1, L, 1, d))
+        held = Held(k * size, v, "int8", 64, bf16)
+        q = rounded(rng.standard_normal((1, 1, 1, d)) / size, bf16)
+        o, lse = held.attend(q, 1)
+        wo, wl, w = held.wanted(q, 1)
+        z_abs = (np.abs(q[0, 0].astype(np.float64)) @ np.abs(held.k[0, :, 0]).T).max() * d ** -0.5
+        dz = ((d + 16) * 2.0 ** -24 + (0 if bf16 else 2.0 ** -22)) * z_abs + 4 * 2.0 ** -24 * (z_abs + 16)
+        sums = (L / 8 + 64) * 2.0 ** -24
+        E = (2.0 ** -11 if bf16 else 2.0 ** -21) + 2 * dz + sums
+        v = np.abs(held.v[0, :, 0])
+        tol = E * (w[0, 0] @ v) + L * 2.0 ** -28 * v.max()
+        if bf16:
+            tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(wo[0, 0])
+        assert np.all(np.abs(o[0, 0] - wo[0, 0]) <= tol)
+        assert np.all(np.abs(lse - wl) <= dz + sums + 2.0 ** -22 * np.abs(wl))
