@@ -8,8 +8,8 @@
 // with four consecutive tokens of one row in a lane, and the product O^T = V^T P^T takes
 // its eight tokens a lane in any order, so with values stored by quads of tokens the weights go
 // straight from registers back into the matrix unit: no lane exchange but the row maximum.
-// Value scales multiply the weights (they belong to a token and a channel group), in units of a
-// running power of two over every value scale seen, so that they fit fp16.
+// Value scales multiply the weights (they belong to a token and a channel group), in a running power of
+// two of the row and group, so that they fit fp16 (see Sums).
 // The softmax keeps a running maximum that may lag by kLag octaves (weights up to
 // 2^(kLift + kLag), which fp16 holds), so accumulators are rescaled only when it is exceeded.
 //
@@ -346,13 +346,32 @@ struct Rows {
 };
 
 // Running softmax and outputs of a wave's rows.
+//
+// A weight times a value scale has to fit fp16 and keep its bits there, so it is taken over a unit: a power
+// of two for each row and channel group, set 2^3 under the largest such product that the row has met
+// and grown only when one would pass 2^15.  It comes from what the row sees: a token that it does not see, or
+// hardly weighs, costs it nothing, however large its values.
+// Finding those products takes every weight, so steps are let through by bounds that cost less: scales of at
+// most a unit (weights are at most 2^15), then the row's largest weight times the lane's largest scale.
+// (Sums of weights over the least unit stay in fp32 up to 2^21 tokens, and products keep their bits
+// down to value scales of 2^-118.)
+constexpr float kMostProduct = 0x1p15f;
+constexpr uint32_t kLeastUnit = (127u - 96u) << 23;     // 2^-96, as are units before any token
 template <class S, int RT>
 struct Sums {
   static constexpr int NJ = S::NB * 2;
-  float4_t acc[RT][NJ];   // [t][2 B + e][i]: channel 32 B + 2 (4 g + i) + e of row n
-  float m[RT], l[RT];     // running maximum (base 2, all lanes of a row agree), sum of this lane
-  float vunit, vinv;      // the running power of two over the value scales, its inverse
-  bool far;               // some row's maximum is past kFar (all lanes agree)
+  // One group: the exponential itself divides by the unit, which costs nothing.  Its argument grows by
+  // the unit's octaves, so not for fp32, whose weights keep 22 bits.
+  static constexpr bool FOLD = S::NG == 1 && S::PIECES == 1;
+  float4_t acc[RT][NJ];   // [t][2 B + e][i]: channel 32 B + 2 (4 g + i) + e of row n, over its unit
+  float m[RT], l[RT];     // running maximum (base 2, all lanes of a row agree), sum of this lane's weights
+  float iu[RT][S::NG];    // one over the unit, in weights under the present m
+  uint32_t room[S::NG];   // the smaller unit of the lane's rows, as bf16 in both halves
+  float base[RT];         // weights are exp2(cs s + base)
+  bool far;               // scores are rounded first (see weigh), by
+  float far_cs[RT];       // this cs; cs is 1 then
+
+  static __device__ float over(float pow2) { return __uint_as_float(0x7F000000u - __float_as_uint(pow2)); }
 
   __device__ void clear() {
 #pragma unroll
@@ -360,17 +379,22 @@ struct Sums {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[t][j] = float4_t{0, 0, 0, 0};
       m[t] = kFloor;
-      l[t] = 0.f;
+      l[t] = base[t] = 0.f;
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G) iu[t][G] = over(__uint_as_float(kLeastUnit));
     }
-    vunit = vinv = 0.f;
+#pragma unroll
+    for (int G = 0; G < S::NG; ++G) room[G] = (kLeastUnit >> 16) * 0x10001u;
     far = false;
   }
 
-  // New maxima: s[t] holds scores over cs, vmax a bound of the step's value scales (all lanes).
+  // log2 of what the weights of row tile t carry beside themselves.
+  __device__ float carried(int t) const {
+    return FOLD ? (float)((int)(__float_as_uint(iu[t][0]) >> 23) - 127) : 0.f;
+  }
   template <int N>
-  __device__ void rescale(const float (&s)[RT][N], const float (&cs)[RT], float vmax) {
-    float mx[RT];
-    bool grow = vmax > vunit;
+  __device__ bool maxima(const float (&s)[RT][N], const float (&cs)[RT], float (&mx)[RT]) const {
+    bool grow = false;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       float x = s[t][0];
@@ -379,59 +403,131 @@ struct Sums {
       mx[t] = rows_max(x) * cs[t];
       grow |= mx[t] > m[t] + kLag;
     }
-    if (!__any(grow)) return;
-    float vf = 1.f;
-    if (vmax > vunit) {
-      // a power of two over vmax with two octaves to spare (value scales end at 2^125)
-      const uint32_t e = min((__float_as_uint(vmax) >> 23) + 3u, 253u);
-      const float now = __uint_as_float(e << 23);
-      vinv = __uint_as_float((254u - e) << 23);
-      vf = vunit * vinv;
-      vunit = now;
+    return grow;
+  }
+
+  // New maxima and units for a step: s[t] holds scores over cs, vs the value scales.
+  template <int NT>
+  __device__ void raise(float (&s)[RT][4 * NT], float (&cs)[RT], const Scales<S::NG> (&vs)[NT]) {
+    float mx[RT];
+    bool grow = maxima(s, cs, mx);
+    // scales are not negative: their bf16 patterns compare as integers, two at a time
+    ushort2_t top[S::NG];
+    uint32_t past = 0u;
+#pragma unroll
+    for (int G = 0; G < S::NG; ++G) {
+      top[G] = us2(vs[0].w[G][0]);
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) top[G] = __builtin_elementwise_max(top[G], us2(vs[u].w[G][i]));
+      past |= __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(top[G], us2(room[G])));
     }
-    bool past = false;
+    if (__builtin_expect(!__any(grow || past != 0u || far), 1)) return;
+    if (far) {
+      round_scores(s, far_cs);
+      grow = maxima(s, cs, mx);
+    }
+    bool close = grow;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const float now = fmaxf(m[t], mx[t]);
-      const float f = __builtin_amdgcn_exp2f(m[t] - now);
-      m[t] = now;
-      past |= now != kFloor && fabsf(now) > kFar;
-      l[t] *= f;
-      const float both = f * vf;
+      const float w = __builtin_amdgcn_exp2f((mx[t] - (m[t] - kLift)) + carried(t));
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][j][i] *= both;
+      for (int G = 0; G < S::NG; ++G)
+        close |= w * (FOLD ? 1.f : iu[t][G]) * __uint_as_float((uint32_t)max(top[G][0], top[G][1]) << 16) > kMostProduct;
     }
-    far = __any(past);
+    if (__any(close)) refit(s, cs, vs, mx);
+    if (far) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i) s[t][i] -= m[t] - kLift;
+    }
+  }
+
+  // Maxima and units from this step's scores, of which mx are the largest.
+  template <int NT>
+  __device__ void refit(float (&s)[RT][4 * NT], float (&cs)[RT], const Scales<S::NG> (&vs)[NT], const float (&mx)[RT]) {
+    float f[RT];
+    bool beyond = false;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      // whole octaves, so that nothing below rounds
+      const float now = mx[t] > m[t] + kLag ? __builtin_ceilf(mx[t]) : m[t];
+      f[t] = __builtin_amdgcn_ldexpf(1.f, (int)fmaxf(m[t] - now, -300.f));
+      m[t] = now;
+      if (!FOLD) l[t] *= f[t];
+      beyond |= now != kFloor && fabsf(now) > kFar;
+    }
+    if (!far && __any(beyond)) {
+      far = true;
+      round_scores(s, cs);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        far_cs[t] = cs[t];
+        cs[t] = 1.f;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float most[S::NG];                     // the largest products over 2^16, which would pass fp32 at 2^127
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G) most[G] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * NT; ++i) {
+        const float w = __builtin_amdgcn_exp2f(fmaf(s[t][i], cs[t], -m[t]) + (kLift - 16.f));
+#pragma unroll
+        for (int G = 0; G < S::NG; ++G) most[G] = fmaxf(most[G], w * vs[i / 4].get(G, i % 4));
+      }
+#pragma unroll
+      for (int G = 0; G < S::NG; ++G) {
+        const float x = rows_max(most[G]);
+        const float old = over(iu[t][G]) * f[t];
+        float unit = fmaxf(old, __uint_as_float(kLeastUnit));
+        // (with the maximum the unit moves up as well, or the bounds above would stop every step from then on)
+        if (x > unit * (f[t] < 1.f ? 0x1p-12f : kMostProduct * 0x1p-16f))
+          unit = __uint_as_float(min((__float_as_uint(x) >> 23) + 13u, 253u) << 23);
+        iu[t][G] = over(unit);
+        const float turn = old * iu[t][G];
+        if (FOLD) l[t] *= turn;
+#pragma unroll
+        for (int j = 2 * G * S::BPG; j < 2 * (G + 1) * S::BPG; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][j][i] *= turn;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) base[t] = (far ? 0.f : kLift - m[t]) + carried(t);
+#pragma unroll
+    for (int G = 0; G < S::NG; ++G) {
+      float most = iu[0][G];
+#pragma unroll
+      for (int t = 1; t < RT; ++t) most = fmaxf(most, iu[t][G]);
+      room[G] = (__float_as_uint(over(most)) >> 16) * 0x10001u;
+    }
+  }
+
+  template <int N>
+  static __device__ void round_scores(float (&s)[RT][N], const float (&cs)[RT]) {
+#pragma clang fp contract(off)   // what is taken off them later stays a step of its own
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[t][i] *= cs[t];
   }
 
   // Scores become weights.  The maximum is a rounded score: up to kFar it is off by 2^-4 at most, and one
   // fused step takes it from exact products.  Past that the difference would keep the maximum's rounding,
-  // which soon is more than its own distance to the row (and 2^32 is past any exponent), so that
-  // the products are rounded as the maximum was: the row's largest weighs 1 whatever its size.
+  // which soon is more than its own distance to the row (and 2^32 is past any exponent).  So from the first
+  // such maximum on the wave's products are rounded first, as the maximum was, and the maximum is
+  // taken off them (raise): the row's largest weighs about 2^kLift whatever its size.
   template <int N>
   __device__ void weigh(float (&s)[RT][N], const float (&cs)[RT]) {
-    if (far) {
-#pragma clang fp contract(off)
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float z = s[t][i] * cs[t];
-          s[t][i] = z - (m[t] - kLift);
-        }
-    } else {
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[t][i] = fmaf(s[t][i], cs[t], kLift - m[t]);
-    }
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        s[t][i] = __builtin_amdgcn_exp2f(s[t][i]);
+        s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], cs[t], base[t]));
         l[t] += s[t][i];
       }
   }
@@ -442,12 +538,12 @@ struct Sums {
     for (int t = 0; t < RT; ++t) {
       float sum = rows_sum(l[t]);
       if (tok[t] < 0) sum = 0.f;     // a row past the drafted tokens saw what it should not have
-      const float inv = is_zero(sum) ? 0.f : vunit / sum;
-      lse[t] = is_zero(sum) ? -INFINITY : m[t] - kLift + __builtin_amdgcn_logf(sum);
+      const float inv = is_zero(sum) ? 0.f : 1.f / sum;
+      lse[t] = is_zero(sum) ? -INFINITY : (m[t] - kLift) + (__builtin_amdgcn_logf(sum) - carried(t));
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][j][i] *= inv;
+        for (int i = 0; i < 4; ++i) acc[t][j][i] = acc[t][j][i] * inv * (FOLD ? 1.f : over(iu[t][j / (2 * S::BPG)]));
     }
   }
 
@@ -536,9 +632,11 @@ __device__ inline void drop_old(Raw<LB>& v, Scales<NG>& s, uint32_t keep) {
   }
 }
 
-// The weights of two tiles (scores at, at + 4) times their value scales, as matrix operands.
+// The weights of two tiles (scores at, at + 4) times their value scales in the rows' units, as matrix
+// operands.  (iu first: a token that the row does not see has a weight of 0 and any scale.)
 template <class S, int KIND, int RT, int N>
-__device__ inline void weight_operands(const float (&s)[RT][N], int at, const float4_t (&sc)[2], half8_t (&pf)[S::PIECES][RT]) {
+__device__ inline void weight_operands(const float (&s)[RT][N], int at, const float4_t (&sc)[2], const float (&iu)[RT],
+                                       half8_t (&pf)[S::PIECES][RT]) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     uint32_t w[4], z[4];
@@ -546,7 +644,7 @@ __device__ inline void weight_operands(const float (&s)[RT][N], int at, const fl
     for (int u = 0; u < 2; ++u) {
       float x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = s[t][at + 4 * u + i] * sc[u][i];
+      for (int i = 0; i < 4; ++i) x[i] = s[t][at + 4 * u + i] * iu[t] * sc[u][i];
       // the token order in which the value codes unpack
       constexpr int o1 = KIND == PACE_CACHE_INT4 ? 2 : 1, o2 = 3 - o1;
       w[2 * u] = pk_f16(x[0], x[o1]);
@@ -563,8 +661,16 @@ __device__ inline void weight_operands(const float (&s)[RT][N], int at, const fl
 
 // ------------------------------------------------------------------------------------ kernel
 
+// Waves a SIMD that the registers have to allow: two for two row tiles with d = 128, where the compiler would stop a
+// few registers short of them.  Those few then are in memory before and after the loop, not in it (a 512-token
+// chunk, int8, g = 32: 318 us, with one wave 444).  Where they would reach into the loop, one wave it is.
+template <int KIND, int D, int GROUP, bool BF16, int RT>
+constexpr int least_waves() {
+  return D == 128 && RT == 2 && !(GROUP == 32 && (!BF16 || KIND == PACE_CACHE_INT4)) ? 2 : 1;
+}
+
 template <int KIND, int D, int GROUP, bool BF16, int RT, int NW>
-__global__ __launch_bounds__(NW * 64) void attn_kernel(AttnParams p) {
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(least_waves<KIND, D, GROUP, BF16, RT>()))) void attn_kernel(AttnParams p) {
   using S = Shape<KIND, D, GROUP, BF16>;
   using C = Codes<KIND>;
   constexpr int NT = kTiles, STEP = 16 * NT;
@@ -666,15 +772,7 @@ __global__ __launch_bounds__(NW * 64) void attn_kernel(AttnParams p) {
       }
     }
 
-    // scales are not negative: their bf16 patterns compare as integers, two at a time
-    ushort2_t top = us2(vs[0].w[0][0]);
-#pragma unroll
-    for (int u = 0; u < NT; ++u)
-#pragma unroll
-      for (int G = 0; G < S::NG; ++G)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) top = __builtin_elementwise_max(top, us2(vs[u].w[G][i]));
-    sums.rescale(s, rows.cs, rows_max(__uint_as_float((uint32_t)max(top[0], top[1]) << 16)));
+    sums.raise(s, rows.cs, vs);
     sums.weigh(s, rows.cs);
 
     // ---- O^T += V^T P^T
@@ -686,9 +784,12 @@ __global__ __launch_bounds__(NW * 64) void attn_kernel(AttnParams p) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[u][i] = vs[2 * pr + u].get(G, i) * sums.vinv;
+          for (int i = 0; i < 4; ++i) sc[u][i] = vs[2 * pr + u].get(G, i);
+        float iu[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) iu[t] = sums.FOLD ? 1.f : sums.iu[t][G];
         half8_t pf[S::PIECES][RT];
-        weight_operands<S, KIND>(s, 8 * pr, sc, pf);
+        weight_operands<S, KIND>(s, 8 * pr, sc, iu, pf);
 #pragma unroll
         for (int jb = 0; jb < S::BPG; ++jb) {
           const int B = G * S::BPG + jb;
