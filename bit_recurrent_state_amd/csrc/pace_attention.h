@@ -831,26 +831,24 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(least_w
     float top = lse[t];
     for (int k = 1; k < NW; ++k) top = fmaxf(top, lds[(size_t)(k - 1) * SLOT + (t * (REGS + 1) + REGS) * 64 + lane]);
     const float base = is_empty(top) ? 0.f : top;
-    float f = __builtin_amdgcn_exp2f(lse[t] - base), sum = f;
+    float sum = __builtin_amdgcn_exp2f(lse[t] - base);
+    for (int k = 1; k < NW; ++k) sum += __builtin_amdgcn_exp2f(lds[(size_t)(k - 1) * SLOT + (t * (REGS + 1) + REGS) * 64 + lane] - base);
+    // shares that add up to 1: outputs of up to 2^127 stay finite
+    const float inv = is_zero(sum) ? 0.f : 1.f / sum;
+    float f = __builtin_amdgcn_exp2f(lse[t] - base) * inv;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sums.acc[t][j][i] *= f;
     for (int k = 1; k < NW; ++k) {
       const float* from = lds + (size_t)(k - 1) * SLOT + t * (REGS + 1) * 64 + lane;
-      f = __builtin_amdgcn_exp2f(from[REGS * 64] - base);
-      sum += f;
+      f = __builtin_amdgcn_exp2f(from[REGS * 64] - base) * inv;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sums.acc[t][j][i] = fmaf(from[(4 * j + i) * 64], f, sums.acc[t][j][i]);
     }
-    const float inv = is_zero(sum) ? 0.f : 1.f / sum;
     lse[t] = is_zero(sum) ? -INFINITY : base + __builtin_amdgcn_logf(sum);
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sums.acc[t][j][i] *= inv;
   }
   sums.store(p, w, row0, lane, lse);
 }

@@ -13,21 +13,21 @@ constexpr int kFewPieces = 16;
 // Four channels of a row and its lse to where the caller wants them.
 template <int D, bool BF16>
 __device__ inline void store_row(const AttnParams& p, int64_t row, int c, float4 acc, float top, float sum) {
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int r = (int)(row % p.R), i = r / p.gamma;
   const int64_t bh = row / p.R, b = bh / p.Hkv, h = bh % p.Hkv;
   const int64_t at = (b * p.T + i) * p.Hq + h * p.gamma + (r - i * p.gamma);
   if (c == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994530942f;
   if constexpr (BF16) {
     auto pack = [&](float x, float y) {
-      return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(x * inv)) |
-             (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(y * inv)) << 16;
+      return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)y) << 16;
     };
     *(uint2*)((uint16_t*)p.o + at * D + 4 * c) = make_uint2(pack(acc.x, acc.y), pack(acc.z, acc.w));
   } else {
-    *(float4*)((float*)p.o + at * D + 4 * c) = float4{acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    *(float4*)((float*)p.o + at * D + 4 * c) = acc;
   }
 }
+
+// Pieces are summed by their shares of the weight, which add up to 1: outputs of up to 2^127 stay finite.
 
 // Few pieces, usually of many rows: D / 4 threads a row, four channels each, which walk the pieces
 // themselves.  (A workgroup a row took 38 us for the 32768 rows of 2 pieces of a 512-token chunk.)
@@ -46,17 +46,22 @@ __global__ __launch_bounds__(kJoin) void join_few_kernel(AttnParams p) {
     top = fmaxf(top, l[s]);
   }
   if (top == -INFINITY) top = 0.f;      // nothing seen (or NaN everywhere)
+#pragma unroll
+  for (int s = 0; s < kFewPieces; ++s) {
+    l[s] = __builtin_amdgcn_exp2f(l[s] - top);
+    sum += l[s];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   float4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s0 = 0; s0 < kFewPieces; s0 += 4) {
     if (s0 >= p.nsplit) break;
 #pragma unroll
     for (int k = 0; k < 4; ++k)         // an empty piece wrote no output
-      o[k] = l[s0 + k] != -INFINITY ? *(const float4*)(p.part_o + ((s0 + k) * rows + row) * D + 4 * c) : float4{0, 0, 0, 0};
+      o[k] = l[s0 + k] != 0.f ? *(const float4*)(p.part_o + ((s0 + k) * rows + row) * D + 4 * c) : float4{0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float f = __builtin_amdgcn_exp2f(l[s0 + k] - top);
-      sum += f;
+      const float f = l[s0 + k] * inv;
       acc.x = fmaf(f, o[k].x, acc.x);
       acc.y = fmaf(f, o[k].y, acc.y);
       acc.z = fmaf(f, o[k].z, acc.z);
@@ -102,10 +107,11 @@ __global__ __launch_bounds__(kJoin) void join_kernel(AttnParams p) {
   __syncthreads();
   sum = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
   const int c = threadIdx.x % C, grp = threadIdx.x / C;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   float4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int s = grp; s < p.nsplit; s += NGRP) {
-    const float f = weight[s];
+    const float f = weight[s] * inv;
     if (f != 0.f) {                     // an empty piece wrote no output
       const float4 o = *(const float4*)(p.part_o + (s * rows + row) * D + 4 * c);
       acc.x = fmaf(f, o.x, acc.x);

@@ -134,3 +134,20 @@ def test_values_that_grow_and_shrink_along_the_context(kind, d, g, bf16):
         v *= 2.0 ** (sign * ramp)[None, :, None, None]
         k[0, :, 0, 0] = 2 * follow * sign * ramp
         check(Held(k, v, kind, g, bf16, gamma), q, T)
+
+
+@pytest.mark.parametrize("kind,d,g", SHAPES)
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("L,max_len", [(150, None), (900, None), (5000, 5000)])
+def test_mean_of_the_largest_values_is_finite(kind, d, g, bf16, L, max_len):
+    """Infinities are held as 2^127: the mean of many is one, not infinite, however the context is cut."""
+    rng = np.random.default_rng(L)
+    v = rng.standard_normal((1, L, 1, d))
+    v[..., 5], v[..., 17] = np.inf, -np.inf
+    held = Held(rng.standard_normal((1, L, 1, d)), v, kind, g, bf16)
+    o, _ = held.attend(np.zeros((1, 1, 1, d), dtype=np.float32), 1, max_len=max_len)
+    want = held.v[0, 0, 0]
+    assert np.all(np.isfinite(o))
+    E = (2.0 ** -8 if bf16 else 0.0) + 2.0 ** -10 + (L / 8 + 64) * 2.0 ** -24
+    for c in (5, 17):
+        assert abs(o[0, 0, 0, c] - want[c]) <= E * abs(want[c])
