@@ -37,11 +37,11 @@ COMMON = [
     "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-I" + os.path.join(ROOT, "include"),
 ]
-# NaN / Inf inputs are undefined by pace.h: min / max need no NaN quieting there (nor in the
-# attention kernels, which test bits where a NaN row matters).  Rotary, the cache and the join of
-# attention's pieces have defined results for them in ordinary comparisons.
+# NaN / Inf inputs are undefined by pace.h: min / max need no NaN quieting there.  The attention
+# layers' operators (pace_cache.h) have defined results for them.
 FINITE_ONLY = ["-fno-honor-nans"]
-HONOR_NANS = {"pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip"}
+HONOR_NANS = {"pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip", "pace_attention_int8.hip",
+              "pace_attention_int4.hip", "pace_attention_fp8.hip"}
 
 
 def _compile(src: str) -> str:

@@ -200,8 +200,7 @@ __device__ inline float rows_sum(float x) {
   return __uint_as_float(a.lo) + __uint_as_float(a.hi);
 }
 __device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-// Bit tests: these sources are compiled with NaNs not honoured in arithmetic, and a NaN row has
-// to stay one.
+// A NaN row stays one: no sum of it is zero, no lse of it is that of an empty row.
 __device__ inline bool is_zero(float x) { return __float_as_uint(x) == 0u; }
 __device__ inline bool is_empty(float lse) { return __float_as_uint(lse) == 0xFF800000u; }
 
@@ -457,7 +456,7 @@ struct Sums {
       f[t] = __builtin_amdgcn_ldexpf(1.f, (int)fmaxf(m[t] - now, -300.f));
       m[t] = now;
       if (!FOLD) l[t] *= f[t];
-      beyond |= now != kFloor && fabsf(now) > kFar;
+      beyond |= fabsf(now) > kFar && fabsf(now) < -kFloor;   // (an infinite query is its own row's affair)
     }
     if (!far && __any(beyond)) {
       far = true;
