@@ -91,15 +91,17 @@ AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   // against 8.2 to 8.9: faster to about 512 tokens, and to 1000 with 16 sequences.)
   a.waves = a.row_tiles == 1 && c.d <= 128 && base <= 256 && max_len > 256 && max_len <= 768 ? 8 : 4;
   a.step = 16 * kTiles * a.waves;
-  // Otherwise pieces until the 256 compute units hold three workgroups each, none under two steps.
+  // Otherwise pieces until the 256 compute units hold three workgroups each, at most one for every two steps
+  // (rounded up to whole steps; the last piece is what is left).
   // (Twice as many cost 6% of three contexts of 131072 tokens and 15% of 16 trees of 25, and
   // gained 2% of 64 ragged ones: every workgroup waits for its first tokens, and its part is written
   // and read once more.)
   const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, 768 / base);
   const int most = ceil_div(max_len, 2 * a.step);
   const int n = (int)std::min<int64_t>(std::min<int64_t>(want, most), kMaxPieces);
-  a.chunk = ceil_div(ceil_div(max_len, n), a.step) * a.step;
-  a.nsplit = ceil_div(max_len, a.chunk);
+  const int64_t chunk = (int64_t)ceil_div(ceil_div(max_len, n), a.step) * a.step;
+  a.nsplit = ceil_div(max_len, chunk);
+  a.chunk = (int)std::min<int64_t>(chunk, INT32_MAX / a.step * a.step);   // (one piece ends with the tokens)
   return a;
 }
 

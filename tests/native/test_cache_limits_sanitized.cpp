@@ -1,0 +1,79 @@
+// Host entry points of the attention-layer operators (csrc/pace_cache.cpp) at the ends of their ranges, built for the
+// CPU with AddressSanitizer and UndefinedBehaviorSanitizer and linked against recording stand-ins of the kernel
+// launchers.  Built and run by tests/test_cache_limits.py; prints "OK <checks>" on success.
+#include <climits>
+#include <cstdio>
+#include <random>
+#include <vector>
+
+#include "../../bit_recurrent_state_amd/csrc/pace_cache_internal.h"
+
+using namespace pace;
+
+static int fails = 0;
+static long checks = 0;
+#define EXPECT(c)                                        \
+  do {                                                   \
+    ++checks;                                            \
+    if (!(c) && fails++ < 30) printf("FAIL line %d: %s\n", __LINE__, #c); \
+  } while (0)
+
+namespace pace {
+static int launches = 0;
+static std::vector<RotaryParams> rot;
+static CacheIoParams io;
+static AttnParams at;
+static AttnPlan at_plan;
+hipError_t launch_rotary(const RotaryParams& p, int, bool, hipStream_t) {
+  ++launches; rot.push_back(p);
+  return hipSuccess;
+}
+hipError_t launch_cache_write(const CacheIoParams& p, int, int, int, int, hipStream_t) {
+  ++launches; io = p;
+  return hipSuccess;
+}
+hipError_t launch_cache_read(const CacheIoParams& p, int, int, int, int, hipStream_t) {
+  ++launches; io = p;
+  return hipSuccess;
+}
+hipError_t launch_attention(const AttnParams& p, const AttnPlan& a, int, int, int, int, hipStream_t) {
+  ++launches; at = p; at_plan = a;
+  return hipSuccess;
+}
+}  // namespace pace
+
+static void* const X = (void*)0x100000;
+static const int32_t* const I = (const int32_t*)0x200000;
+
+// Any max_len that fits its type plans whole pieces that cover it.
+static void plans() {
+  std::mt19937 rng(9);
+  auto pick = [&](std::vector<int> v) { return v[rng() % v.size()]; };
+  const std::vector<int> ends = {INT_MAX, INT_MAX - 1, INT_MAX - 127, INT_MAX - 128, INT_MAX - 255, INT_MAX - 256, INT_MAX - 4096,
+                                 1 << 30, (1 << 30) + 1};
+  for (int trial = 0; trial < 4000; ++trial) {
+    pace_cache_cfg c{};
+    c.B = pick({1, 2, 3, 64, 97, 128, 768, 1000}); c.Hkv = pick({1, 2, 8}); c.Hq = c.Hkv * (1 + rng() % 9);
+    c.d = pick({64, 128, 256}); c.kind = rng() % 3; c.group = pick({32, 64});
+    c.page = pick({16, 64, 1024}); c.num_pages = 1 + rng() % 100000; c.max_pages = 1 + rng() % 20000;
+    c.io_dtype = rng() % 2;
+    const int T = 1 + rng() % 40, max_len = rng() % 2 ? pick(ends) : 1 + (int)(rng() % INT_MAX);
+    size_t need = 0;
+    EXPECT(pace_cache_attention_workspace_bytes(&c, T, max_len, &need) == PACE_OK);
+    const int before = launches;
+    EXPECT(pace_cache_attention(&c, X, I, X, (int64_t)c.Hq * c.d, T, I, nullptr, nullptr, 0, 0.1, max_len, X, nullptr,
+                                need ? X : nullptr, need, nullptr) == PACE_OK);
+    EXPECT(launches == before + 1);
+    EXPECT(at.nsplit >= 1 && at.nsplit <= kMaxPieces && at.chunk > 0 && at.chunk % at_plan.step == 0);
+    // (one piece takes all there is, whatever its length)
+    EXPECT(at.nsplit == 1 || ((int64_t)at.nsplit * at.chunk >= max_len && (int64_t)(at.nsplit - 1) * at.chunk < max_len));
+    EXPECT((need != 0) == (at.nsplit > 1));
+  }
+}
+
+int main() {
+  plans();
+  if (fails) return printf("%d failures\n", fails), 1;
+  printf("OK %ld\n", checks);
+  return 0;
+}
