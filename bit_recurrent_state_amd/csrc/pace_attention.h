@@ -244,7 +244,8 @@ __device__ inline Span span_of(const AttnParams& p, int rows) {
   const int last_row = min((w.rb + 1) * rows, p.R) - 1;
   const int seen = p.tree ? w.drafts : min(w.drafts, last_row / p.gamma + 1);
   w.end = uniform(w.drafts > 0 ? (int)min((int64_t)w.ctx + seen, (int64_t)capacity) : 0);
-  w.lo = uniform(w.split * p.chunk);
+  // (contexts may end 16 tokens under 2^31: no sum of a position and a step is formed before it is known to be less)
+  w.lo = uniform((int)min((int64_t)w.split * p.chunk, (int64_t)w.end));
   w.hi = uniform(w.split == p.nsplit - 1 ? w.end : min(w.end, w.lo + p.chunk));
   return w;
 }
@@ -710,10 +711,11 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(least_w
       vs[u] = load_scales<S::NG>(v + rec.codes + (x.t[u].off / 4 + (g & use)) * (S::NG * 8));
     }
   };
-  const int first = w.lo + wave * STEP;
   constexpr int stride = NW * STEP;
+  const bool any = w.hi - w.lo > wave * STEP;
+  const int first = any ? w.lo + wave * STEP : 0;
   Where cur;
-  if (first < w.hi) {
+  if (any) {
     cur = where(first);
     load_keys(cur, -1);
     load_values(cur, -1);
@@ -725,8 +727,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(least_w
   uint32_t magic = 0x64006400u;
   asm("" : "+v"(magic));
 
-  for (int s0 = first; s0 < w.hi; s0 += stride) {
-    const bool more = s0 + stride < w.hi;
+  bool more = any;
+  for (int s0 = first; more; s0 += stride) {
+    more = w.hi - s0 > stride;
     const int use = more ? -1 : 0;
     const Where next = where(more ? s0 + stride : s0);
 
@@ -762,7 +765,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(least_w
     bool there = true;
 #pragma unroll
     for (int u = 0; u < NT; ++u) there = there && cur.t[u].there;
-    if (s0 + STEP > w.ctx || !there) {
+    if (w.ctx - s0 < STEP || !there) {
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         const int p0 = s0 + 16 * u + 4 * g;
