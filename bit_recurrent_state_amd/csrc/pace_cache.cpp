@@ -22,9 +22,12 @@ size_t io_bytes(int io_dtype) { return io_dtype == PACE_IO_BF16 ? 2 : 4; }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-bool rows_ok(const void* p, int64_t stride, int64_t width, int io_dtype) {
+// n steps of `stride` elements of e bytes stay within any address space.
+bool spans(int64_t n, int64_t stride, int64_t e) { return stride <= (INT64_C(1) << 48) / e / std::max<int64_t>(n, 1); }
+
+bool rows_ok(const void* p, int64_t n, int64_t stride, int64_t width, int io_dtype) {
   const int64_t e = (int64_t)io_bytes(io_dtype);
-  return p && aligned(p, 16) && stride >= width && stride <= (INT64_MAX >> 40) && (stride * e) % 16 == 0;
+  return p && aligned(p, 16) && stride >= width && spans(n, stride, e) && (stride * e) % 16 == 0;
 }
 
 pace_status validate(const pace_cache_cfg* c) {
@@ -169,7 +172,7 @@ pace_status pace_rotary(const pace_rotary_cfg* cfg, int32_t n, const int32_t* po
     if (s.H == 0) continue;
     const int64_t width = (int64_t)s.H * cfg->d;
     if (!s.in || !s.out || s.s_in < width || s.s_out < width) return PACE_EINVAL;
-    if (s.s_in > (INT64_MAX >> 40) || s.s_out > (INT64_MAX >> 40)) return PACE_EINVAL;
+    if (!spans(n, s.s_in, (int64_t)e) || !spans(n, s.s_out, (int64_t)e)) return PACE_EINVAL;
     if (!aligned(s.in, e) || !aligned(s.out, e)) return PACE_EINVAL;
     if (s.in == s.out && s.s_in != s.s_out) return PACE_EINVAL;
     wide = wide && aligned(s.in, 16) && aligned(s.out, 16) && (s.s_in * e) % 16 == 0 && (s.s_out * e) % 16 == 0;
@@ -221,10 +224,10 @@ pace_status pace_cache_write(const pace_cache_cfg* cfg, void* cache, const int32
   if (st != PACE_OK) return st;
   if (T < 0) return PACE_EINVAL;
   if (T == 0) return PACE_OK;
-  const int64_t width = (int64_t)cfg->Hkv * cfg->d;
+  const int64_t width = (int64_t)cfg->Hkv * cfg->d, n = (int64_t)cfg->B * T;
   if (!cache || !page_table || !positions || !aligned(cache, 256) || !aligned(page_table, 4) ||
-      !aligned(positions, 4) || !rows_ok(k, k_stride, width, cfg->io_dtype) ||
-      !rows_ok(v, v_stride, width, cfg->io_dtype))
+      !aligned(positions, 4) || !rows_ok(k, n, k_stride, width, cfg->io_dtype) ||
+      !rows_ok(v, n, v_stride, width, cfg->io_dtype))
     return PACE_EINVAL;
   CacheIoParams p{};
   fill_io(&p, cfg, page_table, positions, T, k_stride, v_stride);
@@ -243,10 +246,10 @@ pace_status pace_cache_read(const pace_cache_cfg* cfg, const void* cache,
   if (st != PACE_OK) return st;
   if (T < 0) return PACE_EINVAL;
   if (T == 0) return PACE_OK;
-  const int64_t width = (int64_t)cfg->Hkv * cfg->d;
+  const int64_t width = (int64_t)cfg->Hkv * cfg->d, n = (int64_t)cfg->B * T;
   if (!cache || !page_table || !positions || !aligned(cache, 256) || !aligned(page_table, 4) ||
-      !aligned(positions, 4) || !rows_ok(k, k_stride, width, cfg->io_dtype) ||
-      !rows_ok(v, v_stride, width, cfg->io_dtype))
+      !aligned(positions, 4) || !rows_ok(k, n, k_stride, width, cfg->io_dtype) ||
+      !rows_ok(v, n, v_stride, width, cfg->io_dtype))
     return PACE_EINVAL;
   CacheIoParams p{};
   fill_io(&p, cfg, page_table, positions, T, k_stride, v_stride);
@@ -294,9 +297,9 @@ pace_status pace_cache_attention(const pace_cache_cfg* cfg, const void* cache,
   if (st != PACE_OK) return st;
   if (!cache || !page_table || !ctx_lens || !o || !aligned(cache, 256) || !aligned(page_table, 4) ||
       !aligned(ctx_lens, 4) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(draft_lens, 4) ||
-      !aligned(tree, 4) || !rows_ok(q, q_stride, (int64_t)cfg->Hq * cfg->d, cfg->io_dtype))
+      !aligned(tree, 4) || !rows_ok(q, (int64_t)cfg->B * T, q_stride, (int64_t)cfg->Hq * cfg->d, cfg->io_dtype))
     return PACE_EINVAL;
-  if (tree_stride < 0 || tree_stride > (INT64_MAX >> 40) || !std::isfinite(scale)) return PACE_EINVAL;
+  if (tree_stride < 0 || !spans(cfg->B, tree_stride, 4) || !std::isfinite(scale)) return PACE_EINVAL;
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return PACE_EINVAL;
   AttnParams p{};
   p.cache = (const uint8_t*)cache;

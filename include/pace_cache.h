@@ -19,7 +19,8 @@
  *
  * I/O tensors (io_dtype fp32 or bf16): element (token n, head h, channel c) of a tensor with
  * token stride `s` (in elements, s >= heads * d) is at n * s + h * d + c; tokens of [B][T]
- * are numbered b * T + t.  The stride lets q, k and v be slices of one projection's output.
+ * are numbered b * T + t.  The stride lets q, k and v be slices of one projection's output, or the
+ * last tokens of long prompts; all tokens together may span up to 2^48 bytes.
  *
  * Quantiser of the cache: the rules of pace.h's symmetric state quantiser on the vector of one
  * (token, head), each group of g contiguous channels with its own scale:

@@ -71,8 +71,46 @@ static void plans() {
   }
 }
 
+// Token strides as wide as a long prompt, up to 2^48 bytes for all tokens.
+static void strides() {
+  pace_cache_cfg c{};
+  c.B = 4; c.Hq = 32; c.Hkv = 32; c.d = 128; c.kind = PACE_CACHE_INT8; c.group = 128; c.page = 64;
+  c.num_pages = 64; c.max_pages = 64; c.io_dtype = PACE_IO_BF16;
+  pace_rotary_cfg r{32, 32, 128, 128, 0, PACE_IO_BF16};
+  for (int T : {1, 5}) {
+    const int64_t most = (INT64_C(1) << 48) / 2 / (4 * T) / 8 * 8;
+    for (int64_t s : {INT64_C(4096), INT64_C(8388608), INT64_C(16777216), INT64_C(1) << 31, most}) {
+      EXPECT(pace_cache_write(&c, X, I, I, T, X, s, X, s, nullptr) == PACE_OK && io.k_stride == s && io.v_stride == s);
+      EXPECT(pace_cache_read(&c, X, I, I, T, X, s, X, s, nullptr) == PACE_OK && io.k_stride == s && io.v_stride == s);
+      EXPECT(pace_cache_attention(&c, X, I, X, s, T, I, nullptr, nullptr, 0, 0.1, 16, X, nullptr, nullptr, 0, nullptr) == PACE_OK &&
+             at.q_stride == s);
+      rot.clear();
+      EXPECT(pace_rotary(&r, 4 * T, I, (const double*)I, 1.0, 0, X, s, X, s, (char*)X + 64, s, (char*)X + 64, s, nullptr) == PACE_OK);
+      EXPECT(rot.size() == 1 && rot[0].q_stride == s && rot[0].k_out_stride == s);
+    }
+    const int n = launches;
+    for (int64_t s : {most + 8, INT64_C(1) << 60, INT64_MAX / 8 * 8, INT64_C(-4096)}) {
+      EXPECT(pace_cache_write(&c, X, I, I, T, X, s, X, 4096, nullptr) == PACE_EINVAL);
+      EXPECT(pace_cache_read(&c, X, I, I, T, X, 4096, X, s, nullptr) == PACE_EINVAL);
+      EXPECT(pace_cache_attention(&c, X, I, X, s, T, I, nullptr, nullptr, 0, 0.1, 16, X, nullptr, nullptr, 0, nullptr) == PACE_EINVAL);
+      EXPECT(pace_rotary(&r, 4 * T, I, (const double*)I, 1.0, 0, X, s, X, 4096, (char*)X + 64, 4096, (char*)X + 64, 4096, nullptr) ==
+             PACE_EINVAL);
+    }
+    EXPECT(launches == n);
+  }
+  // trees of 16384 drafts a sequence: 2^23 words
+  c.Hkv = 32;
+  const int T = 16384;
+  const int64_t words = (int64_t)T * (T / 32);
+  EXPECT(pace_cache_attention(&c, X, I, X, 4096, T, I, nullptr, (const uint32_t*)X, words, 0.1, 16, X, nullptr, nullptr, 0, nullptr) ==
+             PACE_OK && at.tree_stride == words);
+  EXPECT(pace_cache_attention(&c, X, I, X, 4096, T, I, nullptr, (const uint32_t*)X, INT64_C(1) << 45, 0.1, 16, X, nullptr, nullptr, 0,
+                              nullptr) == PACE_EINVAL);
+}
+
 int main() {
   plans();
+  strides();
   if (fails) return printf("%d failures\n", fails), 1;
   printf("OK %ld\n", checks);
   return 0;
