@@ -22,6 +22,9 @@ size_t io_bytes(int io_dtype) { return io_dtype == PACE_IO_BF16 ? 2 : 4; }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Finite in fp32, in which the kernels take it.
+bool fits_f32(double x) { return std::fabs(x) <= (double)0x1.fffffep127f; }
+
 // n steps of `stride` elements of e bytes stay within any address space.
 bool spans(int64_t n, int64_t stride, int64_t e) { return stride <= (INT64_C(1) << 48) / e / std::max<int64_t>(n, 1); }
 
@@ -154,7 +157,7 @@ pace_status pace_rotary(const pace_rotary_cfg* cfg, int32_t n, const int32_t* po
   if (cfg->d < 2 || cfg->d % 2 || cfg->rd < 2 || cfg->rd % 2 || cfg->rd > cfg->d) return PACE_EINVAL;
   if (cfg->interleaved != 0 && cfg->interleaved != 1) return PACE_EINVAL;
   if (cfg->io_dtype != PACE_IO_F32 && cfg->io_dtype != PACE_IO_BF16) return PACE_EINVAL;
-  if (!std::isfinite(magnitude)) return PACE_EINVAL;
+  if (!fits_f32(magnitude)) return PACE_EINVAL;
   if (cfg->d > 1024 || cfg->rd > 512 || cfg->Hq > kMaxQueryHeads || cfg->Hk > kMaxQueryHeads) return PACE_EUNSUPPORTED;
   if (n == 0) return PACE_OK;
   if (!positions || !freqs || !aligned(positions, 4) || !aligned(freqs, 8)) return PACE_EINVAL;
@@ -299,7 +302,7 @@ pace_status pace_cache_attention(const pace_cache_cfg* cfg, const void* cache,
       !aligned(ctx_lens, 4) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(draft_lens, 4) ||
       !aligned(tree, 4) || !rows_ok(q, (int64_t)cfg->B * T, q_stride, (int64_t)cfg->Hq * cfg->d, cfg->io_dtype))
     return PACE_EINVAL;
-  if (tree_stride < 0 || !spans(cfg->B, tree_stride, 4) || !std::isfinite(scale)) return PACE_EINVAL;
+  if (tree_stride < 0 || !spans(cfg->B, tree_stride, 4) || !fits_f32(scale * kLog2e)) return PACE_EINVAL;
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return PACE_EINVAL;
   AttnParams p{};
   p.cache = (const uint8_t*)cache;

@@ -104,8 +104,8 @@ typedef struct {
  * rotated in place (output == input with the same stride); other overlaps are not allowed.
  * Pointers must be aligned to their element (16 bytes with strides of 16 bytes run fastest).
  * n == 0 is allowed and does nothing.
- * Errors: PACE_EINVAL for null pointers, bad sizes or strides, misalignment;
- * PACE_EUNSUPPORTED for d or rd outside the range above. */
+ * Errors: PACE_EINVAL for null pointers, bad sizes or strides, misalignment, a magnitude that is not
+ * finite in fp32; PACE_EUNSUPPORTED for d or rd outside the range above. */
 pace_status pace_rotary(const pace_rotary_cfg* cfg, int32_t n, const int32_t* positions,
                         const double* freqs, double magnitude, int32_t inverse, const void* q,
                         int64_t q_stride, const void* k, int64_t k_stride, void* q_out,
@@ -184,7 +184,7 @@ pace_status pace_tree_bits(const int32_t* parents, int32_t T, uint32_t* bits);
  * workspace: pace_cache_attention_workspace_bytes(cfg, T, max_len) bytes, 256-byte aligned
  * (NULL if 0).
  * Errors: PACE_EINVAL for null pointers, T < 1, max_len < 1, a negative tree_stride, a
- * non-finite scale, a workspace that is too small, misalignment; PACE_EUNSUPPORTED for
+ * scale over 2.3e38 in magnitude or not finite, a workspace that is too small, misalignment; PACE_EUNSUPPORTED for
  * T * Hq / Hkv over 2^24, or more rows or workgroups in all than 2^31 - 1. */
 pace_status pace_cache_attention(const pace_cache_cfg* cfg, const void* cache,
                                  const int32_t* page_table, const void* q, int64_t q_stride,

@@ -2,6 +2,7 @@
 // CPU with AddressSanitizer and UndefinedBehaviorSanitizer and linked against recording stand-ins of the kernel
 // launchers.  Built and run by tests/test_cache_limits.py; prints "OK <checks>" on success.
 #include <climits>
+#include <cmath>
 #include <cstdio>
 #include <random>
 #include <vector>
@@ -108,9 +109,32 @@ static void strides() {
                               nullptr) == PACE_EINVAL);
 }
 
+// Factors that are finite in fp64 and not in fp32, in which the kernels take them.
+static void factors() {
+  pace_cache_cfg c{};
+  c.B = 1; c.Hq = 2; c.Hkv = 1; c.d = 64; c.kind = PACE_CACHE_FP8; c.group = 64; c.page = 16; c.num_pages = 4; c.max_pages = 4;
+  pace_rotary_cfg r{2, 1, 64, 64, 0, PACE_IO_F32};
+  auto attend = [&](double scale) {
+    return pace_cache_attention(&c, X, I, X, 128, 1, I, nullptr, nullptr, 0, scale, 16, X, nullptr, nullptr, 0, nullptr);
+  };
+  auto rotate = [&](double m) {
+    return pace_rotary(&r, 3, I, (const double*)I, m, 0, X, 128, X, 64, (char*)X + 4096, 128, (char*)X + 8192, 64, nullptr);
+  };
+  const int n = launches;
+  for (double x : {1e39, -1e39, 3.5e38, 1e300, -1e300}) {
+    EXPECT(attend(x) == PACE_EINVAL);
+    EXPECT(rotate(x) == PACE_EINVAL);
+  }
+  EXPECT(attend(2.4e38) == PACE_EINVAL);   // finite itself, not as the base-2 factor
+  EXPECT(launches == n);
+  for (double x : {0.0, 1e-300, -0.125, 2.3e38}) EXPECT(attend(x) == PACE_OK && std::isfinite(at.scale_log2e));
+  for (double x : {0.0, 1e-300, -1.0, 3.4e38}) EXPECT(rotate(x) == PACE_OK && std::isfinite(rot.back().magnitude));
+}
+
 int main() {
   plans();
   strides();
+  factors();
   if (fails) return printf("%d failures\n", fails), 1;
   printf("OK %ld\n", checks);
   return 0;
