@@ -15,6 +15,8 @@ namespace {
 constexpr int kMaxQueryHeads = 1024;
 constexpr int kMaxRows = 1 << 24;
 constexpr double kLog2e = 1.4426950408889634074;
+constexpr int64_t kMaxThreads = INT64_C(0xFFFFFFFF);   // of a launch
+constexpr int kRotaryTokens = 1 << 23;                 // of a launch (256 threads each at most)
 
 int cache_bits(int kind) { return kind == PACE_CACHE_INT4 ? 4 : 8; }
 
@@ -65,9 +67,10 @@ pace_status attn_sizes(const pace_cache_cfg* c, int32_t T, int32_t max_len, Attn
   const int64_t R = (int64_t)T * (c->Hq / c->Hkv);
   if (R > kMaxRows) return PACE_EUNSUPPORTED;
   *plan = attn_plan(*c, T, max_len);
-  // grids of the kernel and of the join
+  // the kernel's grid, and the rows that the join counts (pieces are cut for 384 blocks of rows or fewer: its
+  // own grid is small)
   const int64_t groups = (int64_t)plan->nsplit * plan->row_blocks * c->B * c->Hkv;
-  if (groups > INT32_MAX || (int64_t)c->B * c->Hkv * R > INT32_MAX) return PACE_EUNSUPPORTED;
+  if (groups * 64 * plan->waves > kMaxThreads || (int64_t)c->B * c->Hkv * R > INT32_MAX) return PACE_EUNSUPPORTED;
   *bytes = plan->nsplit > 1
                ? (size_t)plan->nsplit * c->B * c->Hkv * (size_t)R * (size_t)(c->d + 1) * sizeof(float)
                : 0;
@@ -191,8 +194,18 @@ pace_status pace_rotary(const pace_rotary_cfg* cfg, int32_t n, const int32_t* po
   p.interleaved = cfg->interleaved;
   p.inverse = inverse != 0;
   p.copy_q = q != q_out; p.copy_k = k != k_out;
-  const hipError_t err = launch_rotary(p, cfg->io_dtype == PACE_IO_BF16, wide, (hipStream_t)stream);
-  return err == hipSuccess ? PACE_OK : PACE_EHIP;
+  for (int32_t done = 0; done < n;) {
+    p.n = std::min(n - done, kRotaryTokens);
+    const hipError_t err = launch_rotary(p, cfg->io_dtype == PACE_IO_BF16, wide, (hipStream_t)stream);
+    if (err != hipSuccess) return PACE_EHIP;
+    if (p.n == n - done) break;
+    done += p.n;
+    p.positions += p.n;
+    auto on = [&](const void* at, int64_t stride) { return (char*)at + (int64_t)p.n * stride * (int64_t)e; };
+    if (cfg->Hq) p.q = on(p.q, q_stride), p.q_out = on(p.q_out, q_out_stride);
+    if (cfg->Hk) p.k = on(p.k, k_stride), p.k_out = on(p.k_out, k_out_stride);
+  }
+  return PACE_OK;
 }
 
 pace_status pace_cache_layout(const pace_cache_cfg* cfg, pace_cache_layout_info* out) {
@@ -227,6 +240,7 @@ pace_status pace_cache_write(const pace_cache_cfg* cfg, void* cache, const int32
   if (st != PACE_OK) return st;
   if (T < 0) return PACE_EINVAL;
   if (T == 0) return PACE_OK;
+  if (cache_io_blocks(cfg->B, T, cfg->Hkv) * 256 > kMaxThreads) return PACE_EUNSUPPORTED;
   const int64_t width = (int64_t)cfg->Hkv * cfg->d, n = (int64_t)cfg->B * T;
   if (!cache || !page_table || !positions || !aligned(cache, 256) || !aligned(page_table, 4) ||
       !aligned(positions, 4) || !rows_ok(k, n, k_stride, width, cfg->io_dtype) ||
@@ -249,6 +263,7 @@ pace_status pace_cache_read(const pace_cache_cfg* cfg, const void* cache,
   if (st != PACE_OK) return st;
   if (T < 0) return PACE_EINVAL;
   if (T == 0) return PACE_OK;
+  if (cache_io_blocks(cfg->B, T, cfg->Hkv) * 256 > kMaxThreads) return PACE_EUNSUPPORTED;
   const int64_t width = (int64_t)cfg->Hkv * cfg->d, n = (int64_t)cfg->B * T;
   if (!cache || !page_table || !positions || !aligned(cache, 256) || !aligned(page_table, 4) ||
       !aligned(positions, 4) || !rows_ok(k, n, k_stride, width, cfg->io_dtype) ||

@@ -48,6 +48,11 @@ struct CacheIoParams {       // pace_cache_write / pace_cache_read
   int32_t B, T, Hkv, page_shift, num_pages, max_pages;
 };
 
+// Tiles of 16 tokens of a call of T (the first token of 16 or more may be at any place of its tile), and
+// workgroups of four tiles.
+inline int cache_io_tiles(int T) { return T < 16 ? 1 : (int)(((int64_t)T + 15 + 15) / 16); }
+inline int64_t cache_io_blocks(int B, int T, int Hkv) { return ((int64_t)B * cache_io_tiles(T) * Hkv + 3) / 4; }
+
 struct AttnParams {
   const uint8_t* cache;
   const int32_t* table;

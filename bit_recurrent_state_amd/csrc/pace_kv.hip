@@ -537,12 +537,8 @@ __global__ __launch_bounds__(kThreads) void read_kernel(CacheIoParams p, int nti
 
 template <bool WRITE, int KIND, int D, int GROUP, typename E>
 hipError_t launch(const CacheIoParams& p, hipStream_t s) {
-  // tiles of 16 tokens; the first token of 16 or more may be at any place of its tile
-  const int ntile = p.T < 16 ? 1 : (int)(((int64_t)p.T + 15 + 15) / 16);
-  const int64_t waves = (int64_t)p.B * ntile * p.Hkv;
-  if (waves > 0x7FFFFFFF - 4) return hipErrorInvalidValue;
-  const int64_t blocks = (waves + 3) / 4;
-  const dim3 grid((uint32_t)blocks, 2);
+  const int ntile = cache_io_tiles(p.T);
+  const dim3 grid((uint32_t)cache_io_blocks(p.B, p.T, p.Hkv), 2);
   if constexpr (WRITE)
     write_kernel<KIND, D, GROUP, E><<<grid, kThreads, 0, s>>>(p, ntile);
   else

@@ -143,7 +143,8 @@ pace_status pace_cache_layout(const pace_cache_cfg* cfg, pace_cache_layout_info*
  * sequences.  A negative position, one past max_pages * P, or one whose page is not there is
  * skipped; the positions of one sequence must differ.  Runs of consecutive positions are
  * stored fastest.  cache must be 256-byte aligned, k and v 16-byte (strides too).
- * T == 0 is allowed and does nothing. */
+ * T == 0 is allowed and does nothing.
+ * PACE_EUNSUPPORTED where B Hkv ceil((T + 15) / 16) (T < 16: B Hkv) is 2^26 or more; reading, too. */
 pace_status pace_cache_write(const pace_cache_cfg* cfg, void* cache, const int32_t* page_table,
                              const int32_t* positions, int32_t T, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, void* stream);
@@ -185,7 +186,8 @@ pace_status pace_tree_bits(const int32_t* parents, int32_t T, uint32_t* bits);
  * (NULL if 0).
  * Errors: PACE_EINVAL for null pointers, T < 1, max_len < 1, a negative tree_stride, a
  * scale over 2.3e38 in magnitude or not finite, a workspace that is too small, misalignment; PACE_EUNSUPPORTED for
- * T * Hq / Hkv over 2^24, or more rows or workgroups in all than 2^31 - 1. */
+ * T * Hq / Hkv over 2^24, 2^31 rows (B T Hq) in all or more, or 2^24 workgroups or more (one for every 16
+ * or 32 rows of a sequence and key/value head, times the pieces of a context where there are few). */
 pace_status pace_cache_attention(const pace_cache_cfg* cfg, const void* cache,
                                  const int32_t* page_table, const void* q, int64_t q_stride,
                                  int32_t T, const int32_t* ctx_lens, const int32_t* draft_lens,

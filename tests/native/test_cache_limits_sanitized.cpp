@@ -131,10 +131,53 @@ static void factors() {
   for (double x : {0.0, 1e-300, -1.0, 3.4e38}) EXPECT(rotate(x) == PACE_OK && std::isfinite(rot.back().magnitude));
 }
 
+// A launch holds fewer than 2^32 threads: longer calls are cut or refused before any launch.
+static void launch_sizes() {
+  for (int wide : {0, 1})
+    for (int n : {1, 8191, 8192, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, (1 << 24) + 3, (1 << 26) + 5, INT_MAX}) {
+      pace_rotary_cfg r{1, 1, wide ? 16 : 2, wide ? 16 : 2, 0, PACE_IO_BF16};
+      const int64_t s = wide ? 16 : 5;
+      rot.clear();
+      char *q = (char*)((uintptr_t)1 << 40), *k = (char*)((uintptr_t)1 << 41), *qo = (char*)((uintptr_t)1 << 42);
+      EXPECT(pace_rotary(&r, n, I, (const double*)I, 1.0, 0, q, s, k, s, qo, s, k, s, nullptr) == PACE_OK);
+      int64_t done = 0;
+      for (const RotaryParams& p : rot) {
+        EXPECT(p.n > 0 && (int64_t)p.n * 256 < (INT64_C(1) << 32));
+        EXPECT(p.positions == I + done && p.q == q + done * s * 2 && p.q_out == qo + done * s * 2);
+        EXPECT(p.k == k + done * s * 2 && p.k_out == p.k && p.copy_q == 1 && p.copy_k == 0);
+        done += p.n;
+      }
+      EXPECT(done == n);
+    }
+  pace_cache_cfg c{};
+  c.B = 65535; c.Hq = 1024; c.Hkv = 1024; c.d = 64; c.kind = PACE_CACHE_INT4; c.group = 64; c.page = 16;
+  c.num_pages = 64; c.max_pages = 64; c.io_dtype = PACE_IO_BF16;
+  auto io_call = [&](int T) {
+    const pace_status a = pace_cache_write(&c, X, I, I, T, X, 65536, X, 65536, nullptr);
+    EXPECT(pace_cache_read(&c, X, I, I, T, X, 65536, X, 65536, nullptr) == a);
+    return a;
+  };
+  auto attend = [&](int T) {
+    size_t need = 1;
+    const pace_status a = pace_cache_attention_workspace_bytes(&c, T, 64, &need);
+    EXPECT(pace_cache_attention(&c, X, I, X, 65536, T, I, nullptr, nullptr, 0, 0.1, 64, X, nullptr, X, need, nullptr) == a);
+    return a;
+  };
+  EXPECT(io_call(1) == PACE_OK && io_call(15) == PACE_OK && io_call(16) == PACE_EUNSUPPORTED);
+  EXPECT(attend(1) == PACE_EUNSUPPORTED);
+  c.B = 16383;
+  EXPECT(attend(1) == PACE_OK && attend(16) == PACE_OK && attend(17) == PACE_EUNSUPPORTED);   // rows by 16
+  c.B = 16384;
+  EXPECT(attend(1) == PACE_EUNSUPPORTED);
+  c.B = 1; c.Hq = c.Hkv = 8;
+  EXPECT(io_call(INT_MAX) == PACE_EUNSUPPORTED && io_call(1 << 26) == PACE_OK);
+}
+
 int main() {
   plans();
   strides();
   factors();
+  launch_sizes();
   if (fails) return printf("%d failures\n", fails), 1;
   printf("OK %ld\n", checks);
   return 0;

@@ -43,3 +43,25 @@ def test_the_last_positions_of_the_largest_table():
         tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(wo)
         assert np.all(np.abs(host(o)[0, i] - wo) <= tol)
         assert np.all(np.abs(host(lse)[0, i] - wl) <= dz + sums + 2.0 ** -22 * np.abs(wl))
+
+
+@pytest.mark.parametrize("n,d,wide", [((1 << 24) + 3, 2, False), ((1 << 26) + 5, 16, True)])
+def test_rotary_of_more_tokens_than_a_launch_holds(n, d, wide):
+    """Cut into launches: the tokens around the cuts and at the ends, against calls of their own."""
+    import bit_recurrent_state_amd as pace
+    print(f"[cache] rotary of {n} tokens", flush=True)
+    cfg = pace.RotaryConfig(Hq=0, Hk=1, d=d, rd=d)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    pos = torch.randint(0, 1 << 20, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    x = torch.randn((n, 1, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    f = dev(pace.rotary_freqs(d)[0])
+    cuts = [0] + list(range(1 << 23, n, 1 << 23)) + [n]
+    parts = []
+    for c in cuts:
+        lo, hi = max(0, c - 300), min(n, c + 300)
+        part = x[lo:hi].clone()
+        pace.rotary(cfg, pos[lo:hi].clone(), f, None, part, None, part)
+        parts.append((lo, hi, part))
+    pace.rotary(cfg, pos, f, None, x, None, x)
+    for lo, hi, part in parts:
+        assert torch.equal(x[lo:hi], part)
