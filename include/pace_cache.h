@@ -95,11 +95,13 @@ typedef struct {
   int32_t io_dtype;      /* pace_io_dtype */
 } pace_rotary_cfg;
 
-/* Rotates q [n][Hq][d] and k [n][Hk][d] by their positions: with a = position * freqs[i]
- * (formed and reduced in fp64, so far positions lose nothing), m = magnitude,
+/* Rotates q [n][Hq][d] and k [n][Hk][d] by their positions: with a = position * freqs[i], m = magnitude,
  *     y_i = m (x_i cos a - x_j sin a),   y_j = m (x_j cos a + x_i sin a)
- * for the pair (i, j); channels from rd on are copied.  inverse != 0 turns by -a (the transpose
- * up to m^2: gradients, or taking keys back).  Rounded once, to the io type.
+ * for the pair (i, j); channels from rd on are copied.  a is formed and reduced to its fraction of a
+ * turn in fp64; the fraction, its cosine and sine and their products with m are fp32.  The outputs are
+ * rounded once, to the io type.
+ * inverse != 0 turns by -a.  With the same m that is the transpose, which takes gradients back; its
+ * inverse, which takes keys back, is the call with 1 / m.
  * positions int32 [n] (any sign), freqs fp64 [rd / 2], both on the device.  A tensor may be
  * rotated in place (output == input with the same stride); other overlaps are not allowed.
  * Pointers must be aligned to their element (16 bytes with strides of 16 bytes run fastest).
