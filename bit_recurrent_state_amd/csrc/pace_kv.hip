@@ -100,7 +100,8 @@ __device__ inline void scale_of(float m, float& s, float& r) {
   r = s > 0.f ? rcp_bf16(s) : 0.f;
 }
 
-// x / s, correctly rounded (r is the correctly rounded reciprocal, the residual exact).  At most
+// x / s, correctly rounded (r is the correctly rounded reciprocal, the residual exact; for scales under
+// 2^-108 the residual ends below the subnormal numbers and the quotient may be a unit off).  At most
 // L in magnitude, since s >= max|x| / L.
 __device__ inline float quotient(float x, float s, float r) {
   const float a = x * r, e = fmaf(-a, s, x);

@@ -27,8 +27,9 @@
  *   M = max|x| of the group, s = bf16 rounded toward +inf of M / L,
  *   int8 (L = 127), int4 (L = 7):  c = round-half-even(x / s) clipped to +-L, x^ = s c;
  *   fp8 (L = 448):  c = x / s rounded to the nearest e4m3 value (ties to even), x^ = s c.
- * x / s is formed in fp32 (correctly rounded; exact ties of bf16 inputs are exact there).  So
- * that a cache holds finite values only: a NaN is stored as 0, |x| is clamped to 2^127, and
+ * x / s is formed in fp32, correctly rounded for scales from 2^-108 on, where exact ties of bf16 inputs
+ * are exact; under that it may be a unit off, so that a value within 2^-22 of a step of a tie may go
+ * either way.  So that a cache holds finite values only: a NaN is stored as 0, |x| is clamped to 2^127, and
  * a group whose scale lies under 2^-126 is stored as zeros (s = 0).
  *
  * CACHE LAYOUT: num_pages pages; page p, key/value head h is a record of
