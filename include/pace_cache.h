@@ -180,9 +180,14 @@ pace_status pace_tree_bits(const int32_t* parents, int32_t T, uint32_t* bits);
  * lse fp32 [B][T][Hq] (may be NULL): ln sum exp(scale q k).  ctx_lens int32 [B] (device),
  * negative = 0.
  * Computed with matrix instructions on exact codes: fp16 operands with fp32 accumulation for
- * bf16 I/O (weights rounded to 11 bits), two-piece operands (22 bits) for fp32 I/O; softmax
- * statistics and outputs are kept in fp32 and rounded once.  The result does not depend on the
- * other sequences, and repeats bit for bit.
+ * bf16 I/O, two-piece operands (22 bits) for fp32 I/O; softmax statistics and outputs are kept in fp32 and
+ * rounded once.  Weights, times their value scales, are rounded to 11 (22) bits in a unit of their row and
+ * channel group; one under 2^-17 (fp32: 2^-5) of the row's largest such product keeps fewer of them, and is
+ * off by at most 2^-28 of that product.  What a row does not see has no part in it.
+ * Scores are right as long as they, and their parts of a group of channels, fit fp32 in base 2 (2.3e38); a
+ * key may hold 2^127.  A query that is not finite makes its own row NaN, and no other.
+ * For one B, T and max_len a result repeats bit for bit and does not depend on the other sequences' lengths
+ * and contents; another B or max_len may cut a context otherwise, which changes the order of its sums.
  * max_len: upper bound of ctx_lens[b] + T that the work is laid out for (host); a longer
  * sequence is still computed in full, only less evenly spread.
  * workspace: pace_cache_attention_workspace_bytes(cfg, T, max_len) bytes, 256-byte aligned
