@@ -192,6 +192,22 @@ __device__ inline Scales<NG> load_scales(const uint8_t* base) {
   return s;
 }
 
+// The larger of two, as the median with `top`, +inf in a register that the compiler cannot look into: fmaxf passes
+// lane swaps' words and merged values through a quieting step first (12 of 297 vector operations of a step of
+// two row tiles).  Of two NaNs it is +inf: a row of them becomes NaN either way.
+__device__ inline float larger(float a, float b, float top) { return __builtin_amdgcn_fmed3f(a, b, top); }
+__device__ inline float opaque_top() {
+  float top = INFINITY;
+  asm("" : "+s"(top));
+  return top;
+}
+// Maximum over a row's four lanes.
+__device__ inline float rows_most(float x, float top) {
+  LanePair a = pair16(__float_as_uint(x));
+  x = larger(__uint_as_float(a.lo), __uint_as_float(a.hi), top);
+  a = pair32(__float_as_uint(x));
+  return larger(__uint_as_float(a.lo), __uint_as_float(a.hi), top);
+}
 // Sum over a row's four lanes.
 __device__ inline float rows_sum(float x) {
   LanePair a = pair16(__float_as_uint(x));
@@ -394,13 +410,14 @@ struct Sums {
   }
   template <int N>
   __device__ bool maxima(const float (&s)[RT][N], const float (&cs)[RT], float (&mx)[RT]) const {
+    const float top = opaque_top();
     bool grow = false;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      float x = s[t][0];
+      float x = larger(s[t][0], s[t][1], top);
 #pragma unroll
-      for (int i = 1; i < N; ++i) x = fmaxf(x, s[t][i]);
-      mx[t] = rows_max(x) * cs[t];
+      for (int i = 2; i < N; ++i) x = fmaxf(x, s[t][i]);
+      mx[t] = rows_most(x, top) * cs[t];
       grow |= mx[t] > m[t] + kLag;
     }
     return grow;
