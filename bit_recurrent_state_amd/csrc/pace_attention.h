@@ -19,18 +19,19 @@
 // contexts are also cut over workgroups, joined by a second kernel (pace_attention.hip); more rows
 // are more workgroups over the same tokens.
 //
-// What bounds it (d = 128, bf16 rows; "busy" from the issue counters over the kernel's cycles).
-// Few rows, 8-bit codes: memory.  3 tokens over 131072, int8: 154 us, 5.3 TB/s, a large copy's rate.
-// Few rows, 4-bit codes: unpacking and latency.  64 tokens over 512 to 8192, g = 64: 89 us, 3.2 TB/s;
-// vector unit 49% busy, waves wait a quarter of their time, 1.2 of them a SIMD on average since the
-// contexts differ.  Many rows: the vector unit.  512 tokens of 2 sequences over 7680, int8: 220 to 234 us, 569
-// to 606 TFLOP/s; vector unit 69% busy, matrix unit 26%; 20 vector operations a score, unpacking among them.
-// Trees between the two: 16 of 25 tokens over 256 to 4096, fp8: 57 us, 222 TFLOP/s, vector unit 44% busy,
-// 1.15 waves a SIMD.
+// What bounds it (d = 128, bf16 rows, calls in a graph over three input sets; "busy" from the issue counters over
+// the kernel's cycles).  Few rows, 8-bit codes: memory.  3 tokens over 131072, int8: 155 us, 5.3 TB/s, a large
+// copy's rate.  Few rows, 4-bit codes: unpacking and latency.  64 tokens over 512 to 8192, g = 64: 87 us, 3.2 TB/s;
+// vector unit 52% busy, waves wait a fifth of their time, 1.1 of them a SIMD on average since the
+// contexts differ.  Many rows: the vector unit.  512 tokens of 2 sequences over 7680, int8: 223 us, 596
+// TFLOP/s; vector unit 74% busy, matrix unit 26%; 22 vector operations a score, unpacking among them.
+// Trees between the two: 16 of 25 tokens over 256 to 4096, fp8: 57 us, 220 TFLOP/s, vector unit 44% busy,
+// 1.16 waves a SIMD.
 //
-// (A kernel that unpacked every token once a workgroup, into LDS, for waves on different rows was 2 to
-// 7% faster for that chunk in int8 and int4 with g >= 64 and in fp32, and slower elsewhere: 2% in
-// fp8, 6% with d = 64, 16% with g = 32, 17 and 27% for chunks of 128 and 64 tokens, 4% for the trees.)
+// (A kernel that unpacked every token once a workgroup, into LDS, for waves on different rows was, before
+// weights had units of their rows, 2 to 7% faster for that chunk in int8 and int4 with g >= 64 and in fp32,
+// and slower elsewhere: 2% in fp8, 6% with d = 64, 16% with g = 32, 17 and 27% for chunks of 128 and 64
+// tokens, 4% for the trees.)
 #pragma once
 
 #include <hip/hip_runtime.h>

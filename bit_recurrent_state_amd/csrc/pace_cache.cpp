@@ -85,25 +85,26 @@ AttnPlan attn_plan(const pace_cache_cfg& c, int T, int max_len) {
   AttnPlan a;
   const int64_t R = (int64_t)T * (c.Hq / c.Hkv);
   // Two row tiles a wave unpack every code once for 32 rows (d = 128, int8: a 512-token chunk over
-  // 7680 tokens 231 us, with one tile 307).  Up to 32 rows that saves nothing and one tile leaves
-  // more waves (16 trees of 5 to 8 tokens over 4096: 25 to 31 us, with two tiles 28 to 34); from there
-  // to 100 rows either may be ahead by up to 25%, evenly on average.  fp32 with d = 128 has twice the
-  // operands: there trees of 9 to 25 tokens, 36 to 100 rows, take 43 to 85 us with one tile and 51 to 87 with
-  // two (8% on average), trees of 48, 95 to 131 against 86 to 123.  d = 256 has no registers for two.
+  // 7680 tokens 240 us, with one tile 305).  Up to 32 rows that saves nothing and one tile leaves
+  // more waves (16 trees of 5 to 8 tokens over 4096: 25 to 31 us, with two tiles 28 to 35); from there
+  // to 100 rows either may be ahead by up to 22% (trees of 9 to 25 tokens, the three kinds: 36 to 73 us with one
+  // tile, 37 to 62 with two, 2% apart on average).  fp32 with d = 128 has twice the operands: there the same
+  // trees take 42 to 88 us with one tile and 48 to 82 with two (9% more on average), trees of 48 tokens 92 to
+  // 113 against 89 to 113.  d = 256 has no registers for two.
   const int one_tile = c.io_dtype == PACE_IO_F32 && c.d == 128 ? 128 : 32;
   a.row_tiles = c.d <= 128 && R > one_tile ? 2 : 1;
   a.row_blocks = ceil_div(R, 16 * a.row_tiles);
   const int64_t base = (int64_t)a.row_blocks * c.B * c.Hkv;
   // Short contexts of few sequences.  Four waves take 256 tokens in one workgroup.  For some more, eight
   // do, and no second kernel has to be launched to join pieces: one sequence of 300 to 760 tokens, 8
-  // heads, takes 8.4 to 9.8 us a call against 11.5.  (In a graph, where launches are cheap, 7.3 to 9.5 us
-  // against 8.2 to 8.9: faster to about 512 tokens, and to 1000 with 16 sequences.)
+  // heads, takes 8.2 to 10.3 us a call against 11.7.  (In a graph, where launches are cheap, 7.5 to 9.9 us
+  // against 8.5 to 9.1: no slower to about 512 tokens, and faster to 1000 with 16 sequences.)
   a.waves = a.row_tiles == 1 && c.d <= 128 && base <= 256 && max_len > 256 && max_len <= 768 ? 8 : 4;
   a.step = 16 * kTiles * a.waves;
   // Otherwise pieces until the 256 compute units hold three workgroups each, at most one for every two steps
   // (rounded up to whole steps; the last piece is what is left).
-  // (Twice as many cost 6% of three contexts of 131072 tokens and 15% of 16 trees of 25, and
-  // gained 2% of 64 ragged ones: every workgroup waits for its first tokens, and its part is written
+  // (Twice as many cost 5% of three contexts of 131072 tokens and 14% of 16 trees of 25, and
+  // gained 3% of 64 ragged ones: every workgroup waits for its first tokens, and its part is written
   // and read once more.)
   const int64_t want = a.waves == 8 ? 1 : std::max<int64_t>(1, 768 / base);
   const int most = ceil_div(max_len, 2 * a.step);

@@ -9,8 +9,8 @@
 // (values).  Runs of consecutive positions are cut at multiples of 16 positions, from any start;
 // a quad that is not whole (single tokens, edges, holes) moves its values byte by byte.
 // Inputs are read once, codes and scales written once.  Writing 4 x 4093 tokens, 8 heads of 128, int4, g =
-// 32: 23 us, 3.7 TB/s; 15 vector operations a value keep that unit 66% busy and waves wait for memory
-// 44% of their time.  Reading them back: 17.6 us, 4.9 TB/s.  Reading 4 x 16384 tokens of int8: 95 us, 4.3
+// 32: 23 us, 3.7 TB/s; 15 vector operations a value keep that unit 67% busy and waves wait
+// 39% of their time.  Reading them back: 17.6 us, 4.9 TB/s.  Reading 4 x 16384 tokens of int8: 95 us, 4.3
 // TB/s; values leave in 4-byte stores, four rows of them a wave.  A token's write takes 3.8 us.
 #include <hip/hip_runtime.h>
 

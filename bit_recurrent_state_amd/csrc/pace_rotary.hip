@@ -124,8 +124,8 @@ void launch(const RotaryParams& p, bool wide, hipStream_t s) {
     rotary_pairs<E><<<p.n, kThreads, p.rd / 2 * sizeof(float2), s>>>(p);
     return;
   }
-  // one token a workgroup while that leaves fewer than eight workgroups a compute unit,
-  // four where the launch is long, so that the angles' barrier is paid once for four tokens
+  // four tokens a workgroup where that still leaves eight workgroups a compute unit, so that the angles'
+  // barrier is paid once for four; one below
   const int tok = p.n >= 4 * 2048 ? 4 : 1;
   const int grid = (p.n + tok - 1) / tok;
   const size_t lds = (size_t)tok * (p.rd / 2) * sizeof(float2);
