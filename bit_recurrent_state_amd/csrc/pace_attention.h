@@ -340,6 +340,7 @@ struct Rows {
       small |= mx > 0.f && e < 126 + 22;
       // the scale's sign goes into q, so that cs > 0 and masks can be -inf
       up = p.scale_log2e == 0.f ? 0.f : copysignf(up, p.scale_log2e);
+      if (mx == INFINITY) up = __builtin_nanf("");   // or scores that are all -inf would pass for masked ones
 #pragma unroll
       for (int B = 0; B < S::NB; ++B) {
         uint32_t u[4], z[4];

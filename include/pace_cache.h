@@ -147,7 +147,7 @@ pace_status pace_cache_layout(const pace_cache_cfg* cfg, pace_cache_layout_info*
  * skipped; the positions of one sequence must differ.  Runs of consecutive positions are
  * stored fastest.  cache must be 256-byte aligned, k and v 16-byte (strides too).
  * T == 0 is allowed and does nothing.
- * PACE_EUNSUPPORTED where B Hkv ceil((T + 15) / 16) (T < 16: B Hkv) is 2^26 or more; reading, too. */
+ * PACE_EUNSUPPORTED where B Hkv ceil((T + 15) / 16) (T < 16: B Hkv) is over 2^26 - 4; reading, too. */
 pace_status pace_cache_write(const pace_cache_cfg* cfg, void* cache, const int32_t* page_table,
                              const int32_t* positions, int32_t T, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, void* stream);

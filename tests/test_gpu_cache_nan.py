@@ -30,3 +30,17 @@ def test_a_query_that_is_not_finite_stays_in_its_row(kind, d, g, bf16, T, gamma,
     keep[T - 1, 1] = False
     assert np.array_equal(o[0][keep], clean[0][keep]) and np.array_equal(l2[0][keep], lse[0][keep])
     assert np.all(np.isnan(o[0, T - 1, 1])) and np.isnan(l2[0, T - 1, 1])
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("T", [1, 40])
+def test_an_infinite_query_whose_scores_are_all_minus_infinity(bf16, T):
+    """It sees tokens, so it is NaN and not a row that sees nothing."""
+    k, v = np.full((1, 45, 1, 64), -1.0), np.ones((1, 45, 1, 64))
+    held = Held(k, v, "int8", 64, bf16)
+    for sign in (1, -1):
+        q = np.ones((1, T, 1, 64), dtype=np.float32)
+        q[0, 0, 0, 3] = sign * np.inf
+        o, lse = held.attend(q, T)
+        assert np.all(np.isnan(o[0, 0])) and np.isnan(lse[0, 0, 0])
+        assert np.all(np.isfinite(o[0, 1:])) and np.all(np.isfinite(lse[0, 1:]))
