@@ -24,7 +24,8 @@ ARCH = "gfx950"
 
 SOURCES = ["pace_host.cpp", "pace_decode.hip", "pace_prefill.hip", "pace_baseline.hip", "pace_calib.hip",
            "pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip", "pace_attention_int8.hip",
-           "pace_attention_int4.hip", "pace_attention_fp8.hip"]
+           "pace_attention_int4.hip", "pace_attention_fp8.hip", "pace_draft.cpp", "pace_draft_step.hip",
+           "pace_draft_commit.hip", "pace_draft_verify.hip", "pace_cache_move.hip"]
 # measurement kernels (include/pace_measure.h), a library of their own
 MEASURE_SOURCES = ["pace_measure.hip"]
 MEASURE_LIB = os.path.join(HERE, "libpace_measure.so")
@@ -38,10 +39,10 @@ COMMON = [
     "-I" + os.path.join(ROOT, "include"),
 ]
 # NaN / Inf inputs are undefined by pace.h: min / max need no NaN quieting there.  The attention
-# layers' operators (pace_cache.h) have defined results for them.
+# layers' operators (pace_cache.h) and the verification of drafts have defined results for them.
 FINITE_ONLY = ["-fno-honor-nans"]
 HONOR_NANS = {"pace_cache.cpp", "pace_rotary.hip", "pace_kv.hip", "pace_attention.hip", "pace_attention_int8.hip",
-              "pace_attention_int4.hip", "pace_attention_fp8.hip"}
+              "pace_attention_int4.hip", "pace_attention_fp8.hip", "pace_draft.cpp", "pace_draft_verify.hip", "pace_cache_move.hip"}
 
 
 def _compile(src: str) -> str:

@@ -77,7 +77,7 @@ struct DecodeParams {
   uint64_t seq_stride;
   uint64_t off_kc, off_ks, off_v, off_vs, off_a, off_beta;  // buffer regions
   int32_t B, Hv, Hk, gamma, dP, group, asym;
-  int32_t flush_only;   // 1: pace_flush_requant (no new token)
+  int32_t flush_only;   // 1: pace_flush_requant (no new token); 2: only buffers that hold dP tokens
   int32_t io_bf16;      // q, k, v, o are bf16 (else fp32)
   int32_t bf16_state;   // the state is bf16 values (one dv x dk record per head)
 };
