@@ -19,6 +19,8 @@
 // Queries enter as they are in bf16, as three bf16 pieces (exact) in fp32.  Everything else is fp32.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "pace_draft_internal.h"
 #include "pace_draft_tokens.h"
 
@@ -45,11 +47,27 @@ struct alignas(16) Smem {
   alignas(16) uint16_t k[NK][TS];               // key codes
   alignas(16) uint16_t q[16 * PIECES][TS];      // one tile of queries
   alignas(16) float u[NK][D];                   // v^, then u
-  alignas(16) float a[NK][NK];                  // [j][i]: beta_i D_ij (k_j . k_i), 0 for j >= i
-  alignas(16) float c[NK][16];                  // [j][i]: D_ij (k_j . q_i) of one tile of queries
-  float scale[4][D], zero[4][D];                // of (group, column)
+  struct Gram {
+    alignas(16) float a[NK][NK];                // [j][i]: beta_i D_ij (k_j . k_i), 0 for j >= i
+    alignas(16) float c[NK][16];                // [j][i]: D_ij (k_j . q_i) of one tile of queries
+  };
+  struct Scales {                               // of (32 keys, column), bf16
+    alignas(16) uint16_t s[D / 32][D];
+    alignas(16) uint16_t z[D / 32][D];          // minus what the operand's codes are too large by
+  };
+  // One tile of tokens is projected before its Gram products are formed, so both fit one place (eight workgroups a
+  // compute unit at D = 128); with more tiles the scales are needed to the end.
+  struct Both {
+    Gram g;
+    Scales s;
+  };
+  union Either {
+    Gram g;
+    Scales s;
+  };
+  alignas(16) std::conditional_t<NKT == 1, Either, Both> m;
   alignas(16) float ks[NK], decay[NK], beta[NK], gamma[NK];
-  uint64_t row[kMaxDrafts];                     // tree bits
+  uint64_t row[NK < kMaxDrafts ? NK : kMaxDrafts];   // tree bits
 };
 
 // The wave's own LDS accesses in order.
@@ -66,14 +84,19 @@ __device__ inline uint4 in_order(const float (&x)[8]) {
   return make_uint4(two_bf16(x[0], x[2]), two_bf16(x[1], x[3]), two_bf16(x[4], x[6]), two_bf16(x[5], x[7]));
 }
 
-template <int D, int NKT, bool BF16, bool BFS>
-__global__ __launch_bounds__(kThreads) void step_kernel(DraftParams p, int mixed) {
+__device__ inline float lane_value(float x, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+
+template <int D, int NKT, bool BF16, bool MIXED, bool BFS>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS && NKT == 1 ? 3 : 1)))
+void step_kernel(DraftParams p) {
   constexpr int PIECES = BF16 ? 1 : 3;
   using SM = Smem<D, NKT, PIECES>;
   constexpr int KB = D / 32;                   // matrix instructions along the keys
   constexpr int SPW = D / 16 / kWaves;         // 16-column strips a wave
   constexpr int CW = D / kWaves;               // columns a wave
-  constexpr int LANES = D / 8, ROWS = kThreads / LANES;
+  constexpr int LANES = D / 8, ROWS = kThreads / LANES, PASS = 16 / ROWS;   // passes over 16 tokens
   __shared__ SM sm;
   const DecodeParams& l = p.l;
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, qq = lane >> 4;
@@ -87,38 +110,77 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DraftParams p, int mixed
     h = ((((h >> (3 + lg)) << 3) + (r & 7)) << lg) | (r >> 3);
   }
   const int kh = h / l.gamma, T = p.T;
-  const int len = p.draft_lens ? min(max(p.draft_lens[b], 0), T) : T;
   const size_t bh = (size_t)b * l.Hv + h, tok0 = (size_t)b * T;
-  const int n = min(max(((const int32_t*)l.buffer)[bh], 0), l.dP - 1), N = n + len;
-  // a lane's columns: c0 .. c0 + SPW - 1, one a strip
-  const int c0 = wave * CW + SPW * l16;
+  // Every load up to the barrier is unconditional with an in-bounds index, so that all are on their way
+  // before the first is waited for.
+  const int count = ((const int32_t*)l.buffer)[bh];
+  const int len_raw = p.draft_lens ? p.draft_lens[b] : T;
 
-  auto store_rows = [&](int t, const float (&x)[SPW]) {
-    const size_t at = ((tok0 + t) * l.Hv + h) * D + c0;
-    if constexpr (BF16) {
-      uint32_t w[SPW / 2];
+  // ------------------------------------------------- 16 tokens at a time, 8 channels a lane
+  const int e0 = 8 * (tid % LANES), row0 = tid / LANES;
+  struct Slots {                               // buffered
+    uint32_t k[PASS][2], v[PASS][MIXED ? 4 : 2];
+    float ks[PASS], vs[PASS], a[PASS], beta[PASS];
+  };
+  auto load_slots = [&](int g, Slots& s) {
 #pragma unroll
-      for (int s = 0; s < SPW / 2; ++s) w[s] = two_bf16(x[2 * s], x[2 * s + 1]);
-      if constexpr (SPW == 4) *(uint2*)((uint16_t*)l.o + at) = make_uint2(w[0], w[1]);
-      else *(uint32_t*)((uint16_t*)l.o + at) = w[0];
-    } else {
-      if constexpr (SPW == 4) *(float4*)((float*)l.o + at) = make_float4(x[0], x[1], x[2], x[3]);
-      else *(float2*)((float*)l.o + at) = make_float2(x[0], x[1]);
+    for (int e = 0; e < PASS; ++e) {
+      const int i = min(16 * g + ROWS * e + row0, l.dP - 1);
+      const size_t kslot = ((size_t)b * l.Hk + kh) * l.dP + i, vslot = bh * l.dP + i;
+      if constexpr (MIXED) {
+        s.k[e][0] = *(const uint32_t*)(l.buffer + l.off_kc + kslot * (D / 2) + e0 / 2);
+        const uint4 w = *(const uint4*)(l.buffer + l.off_v + (vslot * D + e0) * 2);
+        s.v[e][0] = w.x; s.v[e][1] = w.y; s.v[e][2] = w.z; s.v[e][3] = w.w;
+      } else {
+        const uint2 w = *(const uint2*)(l.buffer + l.off_kc + kslot * D + e0), x = *(const uint2*)(l.buffer + l.off_v + vslot * D + e0);
+        s.k[e][0] = w.x; s.k[e][1] = w.y;
+        s.v[e][0] = x.x; s.v[e][1] = x.y;
+        s.vs[e] = ((const float*)(l.buffer + l.off_vs))[vslot];
+      }
+      s.ks[e] = ((const float*)(l.buffer + l.off_ks))[kslot];
+      s.a[e] = ((const float*)(l.buffer + l.off_a))[vslot];
+      s.beta[e] = ((const float*)(l.buffer + l.off_beta))[vslot];
     }
   };
-  {
-    const float none[SPW] = {};
-    for (int t = len + qq; t < T; t += 4) store_rows(t, none);
+  struct Drafts {
+    Raw8<BF16> k[PASS], v[PASS];
+    float a[PASS], beta[PASS];
+  };
+  auto load_drafts = [&](int g, Drafts& s) {
+#pragma unroll
+    for (int e = 0; e < PASS; ++e) {
+      const size_t tok = tok0 + min(16 * g + ROWS * e + row0, T - 1);
+      s.k[e].load(l.k, (int64_t)((tok * l.Hk + kh) * D + e0));
+      s.v[e].load(l.v, (int64_t)((tok * l.Hv + h) * D + e0));
+      s.a[e] = l.a[tok * l.Hv + h];
+      s.beta[e] = l.beta[tok * l.Hv + h];
+    }
+  };
+  auto load_queries = [&](int g, Raw8<BF16> (&x)[PASS]) {
+#pragma unroll
+    for (int e = 0; e < PASS; ++e)
+      x[e].load(l.q, (int64_t)(((tok0 + min(16 * g + ROWS * e + row0, T - 1)) * l.Hk + kh) * D + e0));
+  };
+  Slots slots;
+  load_slots(0, slots);
+  Drafts drafts;
+  load_drafts(0, drafts);
+  Raw8<BF16> queries[PASS];
+  load_queries(0, queries);
+  uint64_t bitsrow = ~0ull;
+  if (p.tree) {
+    const int words = (T + 31) / 32;
+    const uint32_t* t = p.tree + b * p.tree_stride + (int64_t)min(tid, T - 1) * words;
+    bitsrow = t[0] | (words > 1 ? (uint64_t)t[words - 1] << 32 : 0ull);
   }
-  if (len == 0) return;
 
   // ------------------------------------------------------------------ state
   const bool is8 = !BFS && ((l.mask8 >> h) & 1ull) != 0, asym = l.asym != 0;
   const int bits = BFS ? 16 : is8 ? 8 : 4;
   const uint64_t below = h ? (l.mask8 & ((1ull << h) - 1ull)) : 0ull;
   const uint8_t* rec = l.state + (uint64_t)b * l.seq_stride + (uint64_t)h * l.rec4 + (uint64_t)__popcll(below) * (l.rec8 - l.rec4);
-  const int group = BFS ? D : l.group, NG = D / group, kpg = group / 32;
-  // the wave's codes: of strip s, column c0 + s, keys 8 qq .. + 7 of every 32 (one unit each)
+  // a lane's columns: c0 .. c0 + SPW - 1, one a strip; their codes of keys 8 qq .. + 7 of every 32 (one unit each)
+  const int c0 = wave * CW + SPW * l16;
   constexpr int AW = BFS ? 4 * KB : 2 * KB;
   uint32_t raw[SPW][AW];
 #pragma unroll
@@ -136,59 +198,94 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DraftParams p, int mixed
         const uint4 v = *(const uint4*)(col + 8 * (qq * KB + kb));
         raw[s][2 * kb] = v.x; raw[s][2 * kb + 1] = v.y; raw[s][2 * kb + 2] = v.z; raw[s][2 * kb + 3] = v.w;
       }
+    } else if constexpr (KB == 4) {
+      const uint4 v = *(const uint4*)(col + 16 * qq);
+      raw[s][0] = v.x; raw[s][1] = v.y; raw[s][2] = v.z; raw[s][3] = v.w;
     } else {
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) raw[s][kb] = ((const uint32_t*)(col + 4 * qq * KB))[kb];
+      const uint2 v = *(const uint2*)(col + 8 * qq);
+      raw[s][0] = v.x; raw[s][1] = v.y;
     }
   }
+  // a thread's column of scales and zero points
+  uint16_t column_s[KB];
+  uint8_t column_z[KB];
+  const int column = min(tid, D - 1);
   if constexpr (!BFS) {
+    const int kpg = l.group / 32, NG = KB / kpg;
     const uint16_t* scales = (const uint16_t*)(rec + (is8 ? l.scales_off8 : l.scales_off4));
     const uint8_t* zeros = rec + (is8 ? l.zeros_off8 : l.zeros_off4);
-    for (int i = tid; i < D * NG; i += kThreads) {
-      const int c = i / NG, g = i - c * NG;
-      sm.scale[g][c] = bf16_to_f32(scales[i]);
-      sm.zero[g][c] = !asym ? (float)(1 << (bits - 1)) : is8 ? (float)zeros[i] : (float)((zeros[i >> 1] >> (4 * (i & 1))) & 15);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const int i = column * NG + kb / kpg;
+      column_s[kb] = scales[i];
+      if (asym) column_z[kb] = is8 ? zeros[i] : (uint8_t)((zeros[i >> 1] >> (4 * (i & 1))) & 15);
     }
   }
 
   // ----------------------------------------------------------------- tokens
-  const int e0 = 8 * (tid % LANES);
-  for (int i0 = 0; i0 < N; i0 += ROWS) {
-    const int i = i0 + tid / LANES;
-    if (i >= N) continue;
-    float kx[8], vx[8], ks;
-    if (i < n) {
-      const size_t kslot = ((size_t)b * l.Hk + kh) * l.dP + i, vslot = bh * l.dP + i;
-      if (mixed) {
-        const uint32_t w = *(const uint32_t*)(l.buffer + l.off_kc + kslot * (D / 2) + e0 / 2);
+  const int len = min(max(len_raw, 0), T), n = min(max(count, 0), l.dP - 1), N = n + len;
+  const int NT = (N + 15) / 16, NR = 16 * NT;        // tiles and rows in use
+  auto store_rows = [&](int t, const float (&x)[SPW]) {
+    const size_t at = ((tok0 + t) * l.Hv + h) * D + c0;
+    if constexpr (BF16) {
+      uint32_t w[SPW / 2];
+#pragma unroll
+      for (int s = 0; s < SPW / 2; ++s) w[s] = two_bf16(x[2 * s], x[2 * s + 1]);
+      if constexpr (SPW == 4) *(uint2*)((uint16_t*)l.o + at) = make_uint2(w[0], w[1]);
+      else *(uint32_t*)((uint16_t*)l.o + at) = w[0];
+    } else {
+      if constexpr (SPW == 4) *(float4*)((float*)l.o + at) = make_float4(x[0], x[1], x[2], x[3]);
+      else *(float2*)((float*)l.o + at) = make_float2(x[0], x[1]);
+    }
+  };
+  if (len < T) {
+    const float none[SPW] = {};
+    for (int t = len + qq; t < T; t += 4) store_rows(t, none);
+    if (len == 0) return;
+  }
+  auto put = [&](int i, const float (&kx)[8], const float (&vx)[8], float ks, float a, float beta) {
+    *(uint4*)&sm.k[i][e0] = in_order<BFS>(kx);
+    *(float4*)&sm.u[i][e0] = make_float4(vx[0], vx[1], vx[2], vx[3]);
+    *(float4*)&sm.u[i][e0 + 4] = make_float4(vx[4], vx[5], vx[6], vx[7]);
+    if (e0 == 0) {
+      sm.ks[i] = ks;
+      sm.decay[i] = a;
+      sm.beta[i] = beta;
+    }
+  };
+  auto take_slots = [&](int g, const Slots& s) {
+#pragma unroll
+    for (int e = 0; e < PASS; ++e) {
+      const int i = 16 * g + ROWS * e + row0;
+      if (i >= n) continue;
+      float kx[8], vx[8];
+      if constexpr (MIXED) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          kx[j] = (float)((int)((w >> (8 * j)) & 15u) - 8);
-          kx[4 + j] = (float)((int)((w >> (8 * j + 4)) & 15u) - 8);
+          kx[j] = (float)((int)((s.k[e][0] >> (8 * j)) & 15u) - 8);
+          kx[4 + j] = (float)((int)((s.k[e][0] >> (8 * j + 4)) & 15u) - 8);
+          vx[2 * j] = bits_f32(s.v[e][j] << 16);
+          vx[2 * j + 1] = bits_f32(s.v[e][j] & 0xFFFF0000u);
         }
-        load8<true>(l.buffer + l.off_v, (int64_t)(vslot * D + e0), vx);
       } else {
-        const uint2 w = *(const uint2*)(l.buffer + l.off_kc + kslot * D + e0);
-        const uint2 x = *(const uint2*)(l.buffer + l.off_v + vslot * D + e0);
-        const float vs = ((const float*)(l.buffer + l.off_vs))[vslot];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          kx[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-          vx[j] = (float)(int8_t)((j < 4 ? x.x : x.y) >> (8 * (j & 3))) * vs;
+          kx[j] = (float)(int8_t)(s.k[e][j / 4] >> (8 * (j & 3)));
+          vx[j] = (float)(int8_t)(s.v[e][j / 4] >> (8 * (j & 3))) * s.vs[e];
         }
       }
-      ks = ((const float*)(l.buffer + l.off_ks))[kslot];
-      if (e0 == 0) {
-        sm.decay[i] = ((const float*)(l.buffer + l.off_a))[vslot];
-        sm.beta[i] = ((const float*)(l.buffer + l.off_beta))[vslot];
-      }
-    } else {
-      const size_t tok = tok0 + (i - n);
-      float x[8];
-      load8<BF16>(l.k, (int64_t)((tok * l.Hk + kh) * D + e0), x);
-      ks = quantise8<LANES>(x, mixed, kx);
-      load8<BF16>(l.v, (int64_t)((tok * l.Hv + h) * D + e0), x);
-      if (mixed) {
+      put(i, kx, vx, s.ks[e], s.a[e], s.beta[e]);
+    }
+  };
+  auto take_drafts = [&](int g, const Drafts& s) {
+#pragma unroll
+    for (int e = 0; e < PASS; ++e) {
+      const int t = 16 * g + ROWS * e + row0;
+      float x[8], kx[8], vx[8];
+      s.k[e].values(x);
+      const float ks = quantise8<LANES>(x, MIXED, kx);
+      s.v[e].values(x);
+      if constexpr (MIXED) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const uint32_t w = two_bf16(x[j], x[j + 1]);
@@ -200,124 +297,197 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DraftParams p, int mixed
 #pragma unroll
         for (int j = 0; j < 8; ++j) vx[j] *= vs;
       }
-      if (e0 == 0) {
-        sm.decay[i] = l.a[tok * l.Hv + h];
-        sm.beta[i] = l.beta[tok * l.Hv + h];
+      if (t < len) put(n + t, kx, vx, ks, s.a[e], s.beta[e]);
+    }
+  };
+  auto take_queries = [&](int g, const Raw8<BF16> (&in)[PASS]) {
+#pragma unroll
+    for (int e = 0; e < PASS; ++e) {
+      const int i = ROWS * e + row0;
+      float x[8];
+      in[e].values(x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 16 * g + i < len ? x[j] : 0.f;
+#pragma unroll
+      for (int c = 0; c < PIECES; ++c) {
+        *(uint4*)&sm.q[16 * c + i][e0] = in_order<BFS>(x);
+        if (c + 1 < PIECES) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const uint32_t w = two_bf16(x[j], x[j + 1]);
+            x[j] -= bits_f32(w << 16);
+            x[j + 1] -= bits_f32(w & 0xFFFF0000u);
+          }
+        }
       }
     }
-    if (e0 == 0) sm.ks[i] = ks;
-    *(uint4*)&sm.k[i][e0] = in_order<BFS>(kx);
-    *(float4*)&sm.u[i][e0] = make_float4(vx[0], vx[1], vx[2], vx[3]);
-    *(float4*)&sm.u[i][e0 + 4] = make_float4(vx[4], vx[5], vx[6], vx[7]);
+  };
+  take_slots(0, slots);
+  take_drafts(0, drafts);
+  take_queries(0, queries);
+  if constexpr (NKT > 1) {
+    for (int g = 1; 16 * g < n; ++g) {
+      load_slots(g, slots);
+      take_slots(g, slots);
+    }
+    for (int g = 1; 16 * g < len; ++g) {
+      load_drafts(g, drafts);
+      take_drafts(g, drafts);
+    }
   }
-  const int NT = (N + 15) / 16, NR = 16 * NT;        // tiles and rows in use
-  for (int i = N + tid / LANES; i < NR; i += ROWS) { // rows behind the last token hold zeros
+  for (int i = N + row0; i < NR; i += ROWS) {        // rows behind the last token hold zeros
     *(uint4*)&sm.k[i][e0] = make_uint4(0, 0, 0, 0);
     *(float4*)&sm.u[i][e0] = make_float4(0.f, 0.f, 0.f, 0.f);
     *(float4*)&sm.u[i][e0 + 4] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (e0 == 0) sm.ks[i] = sm.decay[i] = sm.beta[i] = 0.f;
   }
-  if (tid < len) {
-    uint64_t bitsrow = ~0ull;
-    if (p.tree) {
-      const int words = (T + 31) / 32;
-      const uint32_t* t = p.tree + b * p.tree_stride + (int64_t)tid * words;
-      bitsrow = t[0];
-      if (words > 1) bitsrow |= (uint64_t)t[1] << 32;
+  if (tid < len) sm.row[tid] = bitsrow;
+  if constexpr (!BFS) {
+    if (tid < D) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        sm.m.s.s[kb][tid] = column_s[kb];
+        const float z = asym ? (float)column_z[kb] : (float)(1 << (bits - 1));
+        sm.m.s.z[kb][tid] = (uint16_t)two_bf16(-((is8 ? 0.f : 16.f) + z), 0.f);
+      }
     }
-    sm.row[tid] = bitsrow;
   }
   __syncthreads();
 
-  // ----------------------------------------------------------------- decays
-  // a[j][i] = D_ij of the tokens before i on its path, 0 elsewhere
-  if (tid < NR) {
-    const int i = tid;
-    float prod = sm.decay[i];
-    const uint64_t bitsrow = i >= n && i < N ? sm.row[i - n] : ~0ull;
-    for (int j = NR - 1; j >= 0; --j) {
-      const bool on = i < N && j < i && (j < n || ((bitsrow >> (j - n)) & 1ull));
-      sm.a[j][i] = on ? prod : 0.f;
-      if (on) prod *= sm.decay[j];
-    }
-    sm.gamma[i] = prod;
-  }
-  __syncthreads();
-
-  // ------------------------------------------------------------------- Gram
+  // ------------------------------------------------------------- projections
   auto operand = [&](const uint16_t* row) { return *(const v8bf*)(row + 8 * qq); };
-  for (int t = wave; t < NT * NT; t += kWaves) {
-    const int it = t / NT, jt = t % NT;               // rows (A) i, columns (B) j
-    if (jt > it) continue;
+  // Of 16 tokens (P operands for every 32 keys) on the wave's columns: x[s] of strip s, tokens 4 qq + r.
+  auto project = [&](auto pieces, auto eight_bits, const uint16_t* rows, v4f (&x)[SPW]) {
+    constexpr int P = decltype(pieces)::value;
+    constexpr bool E8 = decltype(eight_bits)::value;
+#pragma unroll
+    for (int s = 0; s < SPW; ++s) x[s] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      v8bf tok[P];
+#pragma unroll
+      for (int e = 0; e < P; ++e) tok[e] = operand(rows + (size_t)(16 * e + l16) * SM::TS + 32 * kb);
+      if constexpr (BFS) {
+#pragma unroll
+        for (int s = 0; s < SPW; ++s)
+#pragma unroll
+          for (int e = 0; e < P; ++e)
+            x[s] = mfma(tok[e], as_operand(raw[s][4 * kb], raw[s][4 * kb + 1], raw[s][4 * kb + 2], raw[s][4 * kb + 3]), x[s]);
+        continue;
+      }
+      uint32_t sc[SPW / 2], zp[SPW / 2];       // of the lane's columns
+#pragma unroll
+      for (int s = 0; s < SPW / 2; ++s) {
+        sc[s] = *(const uint32_t*)&sm.m.s.s[kb][c0 + 2 * s];
+        zp[s] = *(const uint32_t*)&sm.m.s.z[kb][c0 + 2 * s];
+      }
+#pragma unroll
+      for (int s = 0; s < SPW; ++s) {
+        // (unpacked where they are used: kept from one use to the next, the operands of a tile are 64 registers)
+#pragma unroll
+        for (int i = 0; i < (E8 ? 2 : 1); ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb + i : kb]));
+        v8bf st;
+        if constexpr (E8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t y = raw[s][2 * kb + e];
+            w[2 * e] = two_bf16((float)(y & 255u), (float)((y >> 16) & 255u));
+            w[2 * e + 1] = two_bf16((float)((y >> 8) & 255u), (float)(y >> 24));
+          }
+          st = as_operand(w[0], w[1], w[2], w[3]);
+        } else {
+          const uint32_t y = raw[s][kb];
+          st = as_operand(((y << 3) & 0x00780078u) | 0x41804180u, ((y >> 5) & 0x00780078u) | 0x41804180u,
+                          ((y >> 1) & 0x00780078u) | 0x41804180u, ((y >> 9) & 0x00780078u) | 0x41804180u);
+        }
+        const uint32_t z = __builtin_amdgcn_perm(zp[s / 2], zp[s / 2], s & 1 ? 0x03020302u : 0x01000100u);
+        v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < P; ++e) acc = mfma(tok[e], as_operand(z, z, z, z), acc);
+#pragma unroll
+        for (int e = 0; e < P; ++e) acc = mfma(tok[e], st, acc);
+        const float scale = bits_f32(s & 1 ? sc[s / 2] & 0xFFFF0000u : sc[s / 2] << 16);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[s][r] = fmaf(scale, acc[r], x[s][r]);
+      }
+    }
+  };
+  auto project_any = [&](auto pieces, const uint16_t* rows, v4f (&x)[SPW]) {
+    if (is8) project(pieces, std::true_type{}, rows, x);
+    else project(pieces, std::false_type{}, rows, x);
+  };
+  v4f xq[SPW], xk[SPW];
+  project_any(std::integral_constant<int, PIECES>{}, &sm.q[0][0], xq);
+  project_any(std::integral_constant<int, 1>{}, &sm.k[0][0], xk);
+  if constexpr (NKT == 1) __syncthreads();     // the scales have been read: the Gram products take their place
+
+  // --------------------------------------------------------- decays and Gram
+  // The products of row i, walked back from its own token by one lane: at[j * stride] = D_ij where j is on its path, else 0.
+  // own: its own token is among them (with 1).  Returns the product of them all.
+  const float decay0 = sm.decay[min(lane, NR - 1)], decay1 = NKT > 4 ? sm.decay[min(64 + lane, NR - 1)] : 0.f;
+  auto walk_back = [&](int i, bool own, float* at, int stride, bool in) {
+    const uint64_t on_path = i >= n && i < N ? sm.row[i - n] : ~0ull;
+    const uint32_t lo = (uint32_t)on_path, hi = (uint32_t)(on_path >> 32);
+    in = in && i < N;
+    float prod = own ? 1.f : sm.decay[min(i, NR - 1)];
+    for (int j = NR - 1; j >= 0; --j) {
+      const float dj = NKT > 4 && j >= 64 ? lane_value(decay1, j - 64) : lane_value(decay0, j);
+      const uint32_t word = j - n >= 32 ? hi : lo;
+      const bool on = in && ((own && j == i) || (j < i && (j < n || ((word >> ((j - n) & 31)) & 1u))));
+      at[j * stride] = on ? prod : 0.f;
+      prod = on ? prod * dj : prod;
+    }
+    return prod;
+  };
+  // a[j][i] of one tile of i and one of j (jt <= it)
+  auto gram_keys = [&](int it, int jt) {
     v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) acc = mfma(operand(&sm.k[16 * it + l16][32 * kb]), operand(&sm.k[16 * jt + l16][32 * kb]), acc);
     const int j = 16 * jt + l16, i = 16 * it + 4 * qq;
-    float4* at = (float4*)&sm.a[j][i];
+    float4* at = (float4*)&sm.m.g.a[j][i];
     const float4 d = *at, ksi = *(const float4*)&sm.ks[i], be = *(const float4*)&sm.beta[i];
     const float kj = sm.ks[j];
     *at = make_float4(d.x * be.x * ksi.x * kj * acc[0], d.y * be.y * ksi.y * kj * acc[1], d.z * be.z * ksi.z * kj * acc[2],
                       d.w * be.w * ksi.w * kj * acc[3]);
+  };
+  // c[j][i] of the tile of queries and one of j
+  auto gram_queries = [&](int jt) {
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int e = 0; e < PIECES; ++e)
+        acc = mfma(operand(&sm.q[16 * e + l16][32 * kb]), operand(&sm.k[16 * jt + l16][32 * kb]), acc);
+    const int j = 16 * jt + l16;
+    float4* at = (float4*)&sm.m.g.c[j][4 * qq];
+    const float4 d = *at;
+    const float kj = sm.ks[j];
+    *at = make_float4(d.x * kj * acc[0], d.y * kj * acc[1], d.z * kj * acc[2], d.w * kj * acc[3]);
+  };
+  if constexpr (NKT == 1) {
+    // one wave the keys', the other the queries'
+    if (wave == 0) {
+      if (lane < 16) sm.gamma[lane] = walk_back(lane, false, &sm.m.g.a[0][lane], SM::NK, true);
+      wave_sync();
+      gram_keys(0, 0);
+    } else {
+      if (lane < 16) walk_back(n + lane, true, &sm.m.g.c[0][lane], 16, lane < len);
+      wave_sync();
+      gram_queries(0);
+    }
+  } else {
+    for (int i0 = 64 * wave; i0 < NR; i0 += 64 * kWaves)
+      if (i0 + lane < NR) sm.gamma[i0 + lane] = walk_back(i0 + lane, false, &sm.m.g.a[0][i0 + lane], SM::NK, true);
+    __syncthreads();
+    for (int t = wave; t < NT * NT; t += kWaves) {
+      const int it = t / NT, jt = t % NT;
+      if (jt <= it) gram_keys(it, jt);
+    }
   }
 
-  // State operand of strip s, instruction kb, and the offset it carries.
-  auto state_operand = [&](int s, int kb) {
-    if constexpr (BFS) return as_operand(raw[s][4 * kb], raw[s][4 * kb + 1], raw[s][4 * kb + 2], raw[s][4 * kb + 3]);
-    if (!is8) {
-      const uint32_t x = raw[s][kb];
-      return as_operand(((x << 3) & 0x00780078u) | 0x41804180u, ((x >> 5) & 0x00780078u) | 0x41804180u,
-                        ((x >> 1) & 0x00780078u) | 0x41804180u, ((x >> 9) & 0x00780078u) | 0x41804180u);
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint32_t x = raw[s][2 * kb + e];
-      w[2 * e] = two_bf16((float)(x & 255u), (float)((x >> 16) & 255u));
-      w[2 * e + 1] = two_bf16((float)((x >> 8) & 255u), (float)(x >> 24));
-    }
-    return as_operand(w[0], w[1], w[2], w[3]);
-  };
-  // Projections of 16 tokens (PIECES operands a 32-key block) on the wave's columns: x[s][r] of token 4 qq + r.
-  auto project = [&](auto pieces, const uint16_t* rows, float (&x)[SPW][4]) {
-    constexpr int P = decltype(pieces)::value;
-    v8bf tok[P][KB];
-#pragma unroll
-    for (int e = 0; e < P; ++e)
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) tok[e][kb] = operand(rows + (size_t)(16 * e + l16) * SM::TS + 32 * kb);
-#pragma unroll
-    for (int s = 0; s < SPW; ++s) {
-      v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[s][r] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const v8bf st = state_operand(s, kb);
-        const int g = kb / kpg;
-        if constexpr (!BFS) {
-          const float off = -((is8 ? 0.f : 16.f) + sm.zero[g][c0 + s]);
-          const uint32_t w = two_bf16(off, off);
-          const v8bf z = as_operand(w, w, w, w);
-#pragma unroll
-          for (int e = 0; e < P; ++e) acc = mfma(tok[e][kb], z, acc);
-        }
-#pragma unroll
-        for (int e = 0; e < P; ++e) acc = mfma(tok[e][kb], st, acc);
-        if constexpr (!BFS) {
-          if ((kb + 1) % kpg == 0) {
-            const float sc = sm.scale[g][c0 + s];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[s][r] += sc * acc[r];
-            acc = v4f{0.f, 0.f, 0.f, 0.f};
-          }
-        }
-      }
-      if constexpr (BFS)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[s][r] = acc[r];
-    }
-  };
-  auto add_columns = [&](const float* row, float (&y)[SPW]) {
+  auto columns = [&](const float* row, float (&y)[SPW]) {
     if constexpr (SPW == 4) {
       const float4 v = *(const float4*)(row + c0);
       y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
@@ -326,38 +496,40 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DraftParams p, int mixed
       y[0] = v.x; y[1] = v.y;
     }
   };
+  // x += what the tokens below `end` add, four an instruction (fp32): weights at[j * stride + l16], times sign
+  auto add_tokens = [&](int end, const float* at, int stride, float sign, v4f (&x)[SPW]) {
+    for (int j = qq; j < end + qq; j += 4) {
+      const float w = sign * at[j * stride + l16];
+      float u[SPW];
+      columns(sm.u[j], u);
+#pragma unroll
+      for (int s = 0; s < SPW; ++s) x[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, u[s], x[s], 0, 0, 0);
+    }
+  };
+  if constexpr (NKT > 1) {
+    // (the first tile of queries' decays; their Gram products wait for the barrier)
+    if (wave == 1 && lane < 16) walk_back(n + lane, true, &sm.m.g.c[0][lane], 16, lane < len);
+  }
   __syncthreads();
 
   // ------------------------------------------------------------------ solve
   for (int t = 0; t < NT; ++t) {
-    float x[SPW][4];
-    project(std::integral_constant<int, 1>{}, &sm.k[16 * t][0], x);
+    if (t > 0) project_any(std::integral_constant<int, 1>{}, &sm.k[16 * t][0], xk);
     const int i0 = 16 * t + 4 * qq;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float be = sm.beta[i0 + r], f = be * sm.gamma[i0 + r] * sm.ks[i0 + r];
       float v[SPW];
-      add_columns(sm.u[i0 + r], v);
+      columns(sm.u[i0 + r], v);
 #pragma unroll
-      for (int s = 0; s < SPW; ++s) x[s][r] = be * v[s] - f * x[s][r];
+      for (int s = 0; s < SPW; ++s) xk[s][r] = be * v[s] - f * xk[s][r];
     }
-    for (int j = 0; j < 16 * t; ++j) {
-      const float4 a = *(const float4*)&sm.a[j][i0];
-      float u[SPW];
-      add_columns(sm.u[j], u);
-#pragma unroll
-      for (int s = 0; s < SPW; ++s) {
-        x[s][0] -= a.x * u[s];
-        x[s][1] -= a.y * u[s];
-        x[s][2] -= a.z * u[s];
-        x[s][3] -= a.w * u[s];
-      }
-    }
+    if (t > 0) add_tokens(16 * t, &sm.m.g.a[0][16 * t], SM::NK, -1.f, xk);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float* row = &sm.u[i0 + r][c0];
-      if constexpr (SPW == 4) *(float4*)row = make_float4(x[0][r], x[1][r], x[2][r], x[3][r]);
-      else *(float2*)row = make_float2(x[0][r], x[1][r]);
+      if constexpr (SPW == 4) *(float4*)row = make_float4(xk[0][r], xk[1][r], xk[2][r], xk[3][r]);
+      else *(float2*)row = make_float2(xk[0][r], xk[1][r]);
     }
     wave_sync();
     if (lane < CW) {
@@ -367,7 +539,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DraftParams p, int mixed
       for (int i = 0; i < 16; ++i) y[i] = sm.u[16 * t + i][c];
 #pragma unroll
       for (int j = 0; j < 15; ++j) {
-        const float* a = &sm.a[16 * t + j][16 * t];
+        const float* a = &sm.m.g.a[16 * t + j][16 * t];
 #pragma unroll
         for (int i = j + 1; i < 16; ++i) y[i] -= a[i] * y[j];
       }
@@ -379,79 +551,33 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DraftParams p, int mixed
 
   // ---------------------------------------------------------------- outputs
   for (int t0 = 0; t0 < len; t0 += 16) {
-    __syncthreads();
-    for (int i = tid / LANES; i < 16; i += ROWS) {
-      float x[8] = {};
-      if (t0 + i < len) load8<BF16>(l.q, (int64_t)(((tok0 + t0 + i) * l.Hk + kh) * D + e0), x);
-#pragma unroll
-      for (int e = 0; e < PIECES; ++e) {
-        *(uint4*)&sm.q[16 * e + i][e0] = in_order<BFS>(x);
-        if (e + 1 < PIECES) {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const uint32_t w = two_bf16(x[j], x[j + 1]);
-            x[j] -= bits_f32(w << 16);
-            x[j + 1] -= bits_f32(w & 0xFFFF0000u);
-          }
-        }
+    const int end = min(N, n + t0 + 16);
+    if constexpr (NKT > 1) {
+      if (t0 > 0) {
+        __syncthreads();
+        load_queries(t0 / 16, queries);
+        take_queries(t0 / 16, queries);
+        if (wave == 1 && lane < 16) walk_back(n + t0 + lane, true, &sm.m.g.c[0][lane], 16, t0 + lane < len);
+        __syncthreads();
+        project_any(std::integral_constant<int, PIECES>{}, &sm.q[0][0], xq);
       }
+      for (int jt = wave; 16 * jt < end; jt += kWaves) gram_queries(jt);
+      __syncthreads();
     }
-    // decays of these rows, themselves included
-    if (tid < 16) {
-      const int i = n + t0 + tid;
-      const bool in = t0 + tid < len;
-      const uint64_t bitsrow = in ? sm.row[t0 + tid] : 0ull;
-      float prod = 1.f;
-      for (int j = NR - 1; j >= 0; --j) {
-        const bool on = in && (j == i || (j < i && (j < n || ((bitsrow >> (j - n)) & 1ull))));
-        sm.c[j][tid] = on ? prod : 0.f;
-        if (on) prod *= sm.decay[j];
-      }
-    }
-    __syncthreads();
-    const int jt_end = min(NT, (n + t0 + 16 + 15) / 16);
-    for (int jt = wave; jt < jt_end; jt += kWaves) {
-      v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int e = 0; e < PIECES; ++e)
-          acc = mfma(operand(&sm.q[16 * e + l16][32 * kb]), operand(&sm.k[16 * jt + l16][32 * kb]), acc);
-      const int j = 16 * jt + l16;
-      float4* at = (float4*)&sm.c[j][4 * qq];
-      const float4 d = *at;
-      const float kj = sm.ks[j];
-      *at = make_float4(d.x * kj * acc[0], d.y * kj * acc[1], d.z * kj * acc[2], d.w * kj * acc[3]);
-    }
-    float x[SPW][4];
-    project(std::integral_constant<int, PIECES>{}, &sm.q[0][0], x);
-    __syncthreads();
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = t0 + 4 * qq + r;
       const float g = t < len ? sm.gamma[n + t] : 0.f;
 #pragma unroll
-      for (int s = 0; s < SPW; ++s) x[s][r] *= g;
+      for (int s = 0; s < SPW; ++s) xq[s][r] *= g;
     }
-    const int j_end = min(N, n + t0 + 16);
-    for (int j = 0; j < j_end; ++j) {
-      const float4 c = *(const float4*)&sm.c[j][4 * qq];
-      float u[SPW];
-      add_columns(sm.u[j], u);
-#pragma unroll
-      for (int s = 0; s < SPW; ++s) {
-        x[s][0] += c.x * u[s];
-        x[s][1] += c.y * u[s];
-        x[s][2] += c.z * u[s];
-        x[s][3] += c.w * u[s];
-      }
-    }
+    add_tokens(end, &sm.m.g.c[0][0], 16, 1.f, xq);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = t0 + 4 * qq + r;
       float y[SPW];
 #pragma unroll
-      for (int s = 0; s < SPW; ++s) y[s] = x[s][r];
+      for (int s = 0; s < SPW; ++s) y[s] = xq[s][r];
       if (t < len) store_rows(t, y);
     }
   }
@@ -460,11 +586,12 @@ __global__ __launch_bounds__(kThreads) void step_kernel(DraftParams p, int mixed
 template <int D, int NKT, bool BF16>
 hipError_t launch(const DraftParams& p, int buf_kind, hipStream_t s) {
   const dim3 grid((unsigned)p.l.Hv, (unsigned)p.l.B);
-  const int mixed = buf_kind == PACE_BUF_K4_VBF16;
-  if (p.l.bf16_state)
-    step_kernel<D, NKT, BF16, true><<<grid, kThreads, 0, s>>>(p, mixed);
+  if (p.l.bf16_state)                          // (int8 buffer only: checked by the caller)
+    step_kernel<D, NKT, BF16, false, true><<<grid, kThreads, 0, s>>>(p);
+  else if (buf_kind == PACE_BUF_INT8)
+    step_kernel<D, NKT, BF16, false, false><<<grid, kThreads, 0, s>>>(p);
   else
-    step_kernel<D, NKT, BF16, false><<<grid, kThreads, 0, s>>>(p, mixed);
+    step_kernel<D, NKT, BF16, true, false><<<grid, kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

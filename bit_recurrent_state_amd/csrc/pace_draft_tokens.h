@@ -25,35 +25,56 @@ __device__ inline float token_max(float x) {
   return x;
 }
 
-// Eight neighbouring elements of a q, k or v row.
+// Eight neighbouring elements of a q, k or v row, as they lie in memory.
+template <bool BF16>
+struct Raw8 {
+  uint32_t w[BF16 ? 4 : 8];
+  __device__ void load(const void* p, int64_t at) {
+    const uint4* from = (const uint4*)((const uint8_t*)p + at * (BF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+      const uint4 v = from[i];
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  }
+  __device__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (BF16) x[i] = bits_f32(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+      else x[i] = bits_f32(w[i]);
+    }
+  }
+};
 template <bool BF16>
 __device__ inline void load8(const void* p, int64_t at, float (&x)[8]) {
-  if constexpr (BF16) {
-    const uint4 w = *(const uint4*)((const uint16_t*)p + at);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bits_f32(u[i] << 16);
-      x[2 * i + 1] = bits_f32(u[i] & 0xFFFF0000u);
-    }
-  } else {
-    const float4 a = *(const float4*)((const float*)p + at), b = *(const float4*)((const float*)p + at + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  }
+  Raw8<BF16> r;
+  r.load(p, at);
+  r.values(x);
 }
 
-// Codes (whole numbers) and scale of a token.
+// Codes (whole numbers) and scale of a token.  x / s is formed in three operations from the correctly rounded reciprocal
+// (q = fl(x r) is within an ulp, its residual exact in a fused step, and one more rounds correctly: Markstein), the same
+// fp32 quotient as the decode's division in a quarter of its operations.  Its rounding needs no clamp, since s is at most an
+// ulp under max|x| / top.  A scale whose reciprocal would leave fp32's normal range takes the division.
 template <int LANES>
 __device__ inline float quantise8(const float (&x)[8], bool four_bits, float (&c)[8]) {
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
   m = token_max<LANES>(m);
-  const float top = four_bits ? 7.f : 127.f;
-  const float s = div_rn(m, top, four_bits ? 1.0f / 7.0f : 1.0f / 127.0f);
+  const float s = div_rn(m, four_bits ? 7.f : 127.f, four_bits ? 1.0f / 7.0f : 1.0f / 127.0f);
+  const float r = 1.0f / s;
+  if (__builtin_expect(__any(s < 0x1p-100f), 0)) {
+    const float top = four_bits ? 7.f : 127.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = s > 0.f ? fminf(fmaxf(rintf(x[i] / s), -top), top) : 0.f;
+    for (int i = 0; i < 8; ++i) c[i] = s > 0.f ? fminf(fmaxf(rintf(x[i] / s), -top), top) : 0.f;
+    return s;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = x[i] * r;
+    c[i] = rintf(fmaf(fmaf(-q, s, x[i]), r, q));
+  }
   return s;
 }
 
