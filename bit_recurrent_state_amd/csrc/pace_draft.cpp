@@ -33,7 +33,7 @@ pace_status validate(const pace_verify_cfg* c) {
 
 int verify_chunks(const pace_verify_cfg* c) { return (c->V + kVerifyChunk - 1) / kVerifyChunk; }
 
-size_t verify_bytes(const pace_verify_cfg* c) { return (size_t)c->B * verify_chunks(c) * sizeof(double); }
+size_t verify_bytes(const pace_verify_cfg* c) { return (size_t)c->B * verify_scratch(c->T, verify_chunks(c)); }
 
 }  // namespace
 
@@ -141,9 +141,10 @@ pace_status pace_draft_verify(const pace_verify_cfg* cfg, const void* target, in
   p.uniforms = uniforms;
   p.draft_lens = draft_lens;
   p.nodes = nodes; p.counts = counts; p.next = next;
-  p.sums = (double*)workspace;
+  p.workspace = (uint8_t*)workspace;
   p.B = cfg->B; p.T = cfg->T; p.V = cfg->V;
   p.chunks = verify_chunks(cfg);
+  p.scratch = verify_scratch(cfg->T, p.chunks);
   const hipError_t err = launch_draft_verify(p, cfg->prob_dtype == PACE_IO_BF16, (hipStream_t)stream);
   return err == hipSuccess ? PACE_OK : PACE_EHIP;
 }

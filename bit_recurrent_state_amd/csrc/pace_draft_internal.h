@@ -48,12 +48,16 @@ struct VerifyParams {
   int32_t* nodes;
   int32_t* counts;
   int32_t* next;
-  double* sums;                 // [B][chunks] weights of a row, chunk by chunk
+  uint8_t* workspace;
+  int64_t scratch;              // bytes of a sequence there
   int32_t B, T, V, chunks;
 };
 
 // Tokens of a chunk: what a wave sums at once.
 constexpr int kVerifyChunk = 2048;
+
+// Workspace of a sequence: a double a chunk, the walk (48 bytes), its path and refused tokens.
+inline int64_t verify_scratch(int T, int chunks) { return ((int64_t)chunks * 8 + 48 + 8 * (int64_t)T + 63) / 64 * 64; }
 
 struct MoveParams {
   uint8_t* cache;

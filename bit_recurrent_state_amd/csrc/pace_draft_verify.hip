@@ -1,12 +1,17 @@
 // Verification of drafted tokens (include/pace_draft.h: pace_draft_verify).
 //
-// One workgroup per sequence.  The probabilities of every node's token in its parent's rows are gathered at once; one wave
-// then walks the tree, 64 nodes a ballot.  With A the sum of the W's so far, what is left of a row after its refused children
+// The probabilities of every node's token in its parent's rows are gathered at once; one wave then walks the tree, 64 nodes
+// a ballot.  With A the sum of the W's so far, what is left of a row after its refused children
 // is w = max(p - A q, 0) (the same as taking W q off each time, as q >= 0), so that a row's state is two numbers.
 // A row is read only where its sum is asked for: after a refusal with the draft's probabilities, and to draw the following
 // token.  It is summed in chunks of 2048 tokens, one a wave; the token is found by the chunks' sums and then inside its
 // chunk.  All in fp64: the fp32 (bf16) inputs are exact, and a sum of 2^24 of them is off by 2^-29 of a step of fp32.
+//
+// Few sequences over a large vocabulary: the first row that is asked for is summed by several workgroups a sequence, each
+// of which walks there by itself; a second kernel goes on from there.  Otherwise one workgroup a sequence does it all.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "pace_draft_internal.h"
 #include "pace_numerics.h"
@@ -15,6 +20,7 @@ namespace pace {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kLdsChunks = 128;          // sums that a workgroup keeps to itself
 constexpr int kPer = kVerifyChunk / 64;   // tokens of a chunk a lane holds, eight neighbouring ones at a time
 
 template <typename E>
@@ -23,7 +29,10 @@ struct alignas(sizeof(E)) Eight {
 };
 
 // What a probability counts: 0 for what is none.
-__device__ inline double weight(float x) { return x > 0.f && x <= 3.402823466e38f ? (double)x : 0.0; }
+__device__ inline double weight(float x) {
+  const float y = fmaxf(x, 0.f);         // (of a NaN, too)
+  return (double)(y <= 3.402823466e38f ? y : 0.f);
+}
 __device__ inline double weight(uint16_t x) { return weight(bf16_to_f32(x)); }
 __device__ inline double uniform(float u) { return u > 0.f ? fmin((double)u, 1.0) : 0.0; }
 
@@ -43,30 +52,78 @@ __device__ inline double wave_scan(double x, int lane) {
   return x;
 }
 
-struct Shared {
-  double pt[kMaxNodes], qt[kMaxNodes];   // of a node's token, in its parent's rows of target and draft
-  int32_t parent[kMaxNodes], token[kMaxNodes], path[kMaxNodes];
-  int32_t gone[kMaxNodes];               // draft NULL: tokens of the refused children of x
-  double A, W, u0;
-  int32_t x, at, length, ngone;          // the node, the last child looked at, accepted nodes
-  int32_t sum;                           // the walk waits for the sum of its row
+// The walk's state, and what of it a second kernel needs.
+struct Walk {
+  double A, W;
+  int32_t x, at, length, ngone;          // the node, the last child looked at, accepted nodes, refused ones (draft NULL)
+  int32_t sum, more;                     // the row's sum is waited for; children of x are left behind `at`
 };
 
+static_assert(sizeof(Walk) <= 48, "verify_scratch");
+
+template <int NODES>
+struct Shared {
+  double pt[NODES], qt[NODES], u[NODES]; // of a node's token, in its parent's rows of target and draft; its uniform
+  int32_t parent[NODES], token[NODES], path[NODES];
+  int32_t gone[NODES];                   // draft NULL: tokens of the refused children of x
+  double sums[kLdsChunks];
+  Walk w;
+};
+
+// A sequence's part of the workspace: chunk sums, the walk, its path, refused tokens.
+struct Scratch {
+  double* sums;
+  Walk* w;
+  int32_t *path, *gone;
+};
+__device__ inline Scratch scratch_of(const VerifyParams& p, int b) {
+  uint8_t* const at = p.workspace + (int64_t)b * p.scratch;
+  double* const sums = (double*)at;
+  Walk* const w = (Walk*)(sums + p.chunks);
+  int32_t* const path = (int32_t*)(w + 1);
+  return {sums, w, path, path + p.T};
+}
+
+// Gathers what the walk needs of the nodes, and begins it.
+template <typename E, int NODES>
+__device__ inline int begin(const VerifyParams& p, Shared<NODES>& s, int b, const E* target, const E* draft) {
+  const int tid = threadIdx.x;
+  const int len = p.draft_lens ? min(max(p.draft_lens[b], 0), p.T) : p.T;
+  for (int c = tid; c < p.T; c += blockDim.x) {
+    const int parent = p.parents ? p.parents[b * p.parents_stride + c] : c - 1;
+    const int token = p.tokens[(int64_t)b * p.T + c];
+    const float u = p.uniforms[(int64_t)b * p.T + c];
+    const bool ok = c < len && parent >= 0 && parent < c && token >= 0 && token < p.V;
+    s.parent[c] = ok ? parent : -1;
+    s.token[c] = ok ? token : -1;
+    s.pt[c] = ok ? weight(target[parent * p.target_stride + token]) : 0.0;
+    s.qt[c] = ok && draft ? weight(draft[parent * p.draft_stride + token]) : 0.0;
+    s.u[c] = uniform(u);
+    s.path[c] = 0;
+  }
+  if (tid == 0) s.w = Walk{0.0, 1.0, 0, 0, 1, 0, 0, 0};
+  __syncthreads();
+  return len;
+}
+
 // Goes on with the walk; returns at its end (sum = 0) or where a row's sum is needed (sum = 1).  One wave.
-__device__ inline void walk(const VerifyParams& p, Shared& s, int b, int len, int lane) {
-  const bool drawn = p.draft != nullptr;
-  int x = s.x, at = s.at, length = s.length, ngone = s.ngone;
-  double A = s.A, W = s.W;
-  int sum = 0;
-  for (int blk = (at + 1) / 64; blk * 64 < len && !sum; ++blk) {
+template <int NODES>
+__device__ inline void walk(Shared<NODES>& s, int len, bool drawn, int lane) {
+  int x = s.w.x, at = s.w.at, length = s.w.length, ngone = s.w.ngone;
+  double A = s.w.A, W = s.w.W;
+  int sum = 0, more = 0;
+  for (int blk = (at + 1) / 64; blk * 64 < len && !more; ++blk) {
     const int c = blk * 64 + lane;
     const bool in = c < len;
     const int parent = in ? s.parent[c] : -1, token = in ? s.token[c] : -1;
-    const double pt = in ? s.pt[c] : 0.0, qt = in ? s.qt[c] : 0.0;
-    const double u = in ? uniform(p.uniforms[(int64_t)b * p.T + c]) : 0.0;
+    const double pt = in ? s.pt[c] : 0.0, qt = in ? s.qt[c] : 0.0, u = in ? s.u[c] : 0.0;
     for (;;) {
-      const uint64_t mask = __ballot(c > at && parent == x && token >= 0);
+      const uint64_t mask = __ballot(c > at && parent == x);
       if (!mask) break;
+      if (sum) {                         // (a refusal waits for its row's sum: the next child needs it)
+        more = 1;
+        break;
+      }
       const int l = __builtin_ctzll(mask);
       at = blk * 64 + l;
       const double uc = lane_double(u, l);
@@ -92,7 +149,6 @@ __device__ inline void walk(const VerifyParams& p, Shared& s, int b, int len, in
       } else if (drawn) {
         A += W;
         sum = 1;
-        break;
       } else {
         W = fmax(W - w, 0.0);
         if (lane == 0) s.gone[ngone] = t;
@@ -101,48 +157,52 @@ __device__ inline void walk(const VerifyParams& p, Shared& s, int b, int len, in
       }
     }
   }
-  if (lane == 0) {
-    s.x = x; s.at = at; s.length = length; s.ngone = ngone;
-    s.A = A; s.W = W;
-    s.sum = sum;
-  }
+  if (lane == 0) s.w = Walk{A, W, x, at, length, ngone, sum, more};
 }
 
-// Weights of eight neighbouring tokens of row x.
+// A row of target, less what was refused of it.
 template <typename E>
-__device__ inline void weights(const VerifyParams& p, const Shared& s, const E* pr, const E* qr, double A, int ngone, int v0,
-                               double (&w)[8]) {
+struct Row {
+  const E *p, *q;                        // q null: nothing drawn was refused
+  double A;
+  const int32_t* gone;
+  int ngone, V;
+};
+
+// Weights of eight neighbouring tokens.
+template <typename E>
+__device__ inline void weights(const Row<E>& r, int v0, double (&w)[8]) {
   Eight<E> a, q;
-  if (v0 + 8 <= p.V) {
-    a = *(const Eight<E>*)(pr + v0);
-    if (qr) q = *(const Eight<E>*)(qr + v0);
+  if (v0 + 8 <= r.V) {
+    a = *(const Eight<E>*)(r.p + v0);
+    if (r.q) q = *(const Eight<E>*)(r.q + v0);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      a.v[i] = v0 + i < p.V ? pr[v0 + i] : E(0);
-      if (qr) q.v[i] = v0 + i < p.V ? qr[v0 + i] : E(0);
+      a.v[i] = v0 + i < r.V ? r.p[v0 + i] : E(0);
+      if (r.q) q.v[i] = v0 + i < r.V ? r.q[v0 + i] : E(0);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = qr ? fmax(weight(a.v[i]) - A * weight(q.v[i]), 0.0) : weight(a.v[i]);
-  for (int k = 0; k < ngone; ++k) {
-    const int d = s.gone[k] - v0;
+  for (int i = 0; i < 8; ++i) w[i] = r.q ? fmax(weight(a.v[i]) - r.A * weight(q.v[i]), 0.0) : weight(a.v[i]);
+  for (int k = 0; k < r.ngone; ++k) {
+    const int d = r.gone[k] - v0;
+    if (__any(d >= 0 && d < 8)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (d == i) w[i] = 0.0;
+      for (int i = 0; i < 8; ++i)
+        if (d == i) w[i] = 0.0;
+    }
   }
 }
 
 template <typename E>
-__device__ inline double chunk_sum(const VerifyParams& p, const Shared& s, const E* pr, const E* qr, double A, int ngone,
-                                   int chunk, int lane) {
+__device__ inline double chunk_sum(const Row<E>& r, int chunk, int lane) {
   double sum = 0.0;
 #pragma unroll
   for (int j = 0; j < kPer / 8; ++j) {
     double w[8];
-    weights(p, s, pr, qr, A, ngone, chunk * kVerifyChunk + j * 512 + lane * 8, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += w[i];
+    weights(r, chunk * kVerifyChunk + j * 512 + lane * 8, w);
+    sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
@@ -158,83 +218,22 @@ __device__ inline double total_of(const double* sums, int n, int lane) {
   return t;
 }
 
+// The sums of a row's chunks by the waves of a workgroup, and their total.
 template <typename E>
-__global__ __launch_bounds__(kThreads) void verify_kernel(VerifyParams p) {
-  __shared__ Shared s;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int len = p.draft_lens ? min(max(p.draft_lens[b], 0), p.T) : p.T;
-  if (len == 0) {
-    for (int i = tid; i < p.T; i += kThreads) p.nodes[(int64_t)b * p.T + i] = -1;
-    if (tid == 0) {
-      p.counts[b] = 0;
-      p.next[b] = -1;
-    }
-    return;
-  }
-  const E* const target = (const E*)p.target + (int64_t)b * p.T * p.target_stride;
-  const E* const draft = p.draft ? (const E*)p.draft + (int64_t)b * p.T * p.draft_stride : nullptr;
-  double* const sums = p.sums + (int64_t)b * p.chunks;
-  for (int c = tid; c < len; c += kThreads) {
-    const int parent = p.parents ? p.parents[b * p.parents_stride + c] : c - 1;
-    const int token = p.tokens[(int64_t)b * p.T + c];
-    const bool ok = parent >= 0 && parent < c && token >= 0 && token < p.V;
-    s.parent[c] = ok ? parent : -1;
-    s.token[c] = ok ? token : -1;
-    s.pt[c] = ok ? weight(target[parent * p.target_stride + token]) : 0.0;
-    s.qt[c] = ok && draft ? weight(draft[parent * p.draft_stride + token]) : 0.0;
-    s.path[c] = 0;
-  }
-  if (tid == 0) {
-    s.x = 0; s.at = 0; s.length = 1; s.ngone = 0;
-    s.A = 0.0; s.W = 1.0;
-    s.u0 = uniform(p.uniforms[(int64_t)b * p.T]);
+__device__ inline double row_sums(const VerifyParams& p, const Row<E>& r, double* sums) {
+  const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x >> 6; i < p.chunks; i += blockDim.x / 64) {
+    const double t = chunk_sum(r, i, lane);
+    if (lane == 0) sums[i] = t;
   }
   __syncthreads();
-  double total = 0.0;
-  bool have = false;                  // the sums are those of the walk's row as it is left
-  for (;;) {
-    if (wave == 0) walk(p, s, b, len, lane);
-    __syncthreads();
-    const bool again = s.sum;
-    if (again || !have || s.A == 0.0) {
-      // (a row that was summed has A > 0, and the walk comes to another row with A = 0)
-      const E* const pr = target + s.x * p.target_stride;
-      const E* const qr = draft && s.A > 0.0 ? draft + s.x * p.draft_stride : nullptr;
-      for (int i = wave; i < p.chunks; i += kWaves) {
-        const double t = chunk_sum(p, s, pr, qr, s.A, s.ngone, i, lane);
-        if (lane == 0) sums[i] = t;
-      }
-      __syncthreads();
-      total = total_of(sums, p.chunks, lane);
-    }
-    have = true;
-    if (!again) break;
-    if (tid == 0) s.W = total;
-    __syncthreads();
-  }
-  if (total == 0.0 && (s.A > 0.0 || s.ngone > 0)) {      // nothing is left: the row itself
-    __syncthreads();
-    if (tid == 0) {
-      s.A = 0.0;
-      s.ngone = 0;
-    }
-    __syncthreads();
-    for (int i = wave; i < p.chunks; i += kWaves) {
-      const double t = chunk_sum(p, s, target + s.x * p.target_stride, (const E*)nullptr, 0.0, 0, i, lane);
-      if (lane == 0) sums[i] = t;
-    }
-    __syncthreads();
-    total = total_of(sums, p.chunks, lane);
-  }
-  for (int i = tid; i < p.T; i += kThreads) p.nodes[(int64_t)b * p.T + i] = i < s.length ? s.path[i] : -1;
-  if (tid == 0) p.counts[b] = s.length;
-  if (wave != 0) return;
-  if (total == 0.0) {
-    if (lane == 0) p.next[b] = -1;
-    return;
-  }
-  // the first chunk whose end passes r, or the last of any weight
-  double r = s.u0 * total, before = 0.0, found = 0.0;
+  return total_of(sums, p.chunks, lane);
+}
+
+// The first token whose sum from the row's start passes u total, or the last of any weight.  One wave; total > 0.
+template <typename E>
+__device__ inline int token_at(const VerifyParams& p, const Row<E>& row, const double* sums, double u, double total, int lane) {
+  double r = u * total, before = 0.0, found = 0.0;
   int chunk = -1, last = 0;
   for (int i = 0; i < p.chunks && chunk < 0; i += 64) {
     const double t = i + lane < p.chunks ? sums[i + lane] : 0.0;
@@ -249,19 +248,16 @@ __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyParams p) {
       before = lane_double(upto, 63);
     }
   }
-  if (chunk < 0) {
+  if (chunk < 0) {                       // (u = 1, or a last sum that rounded below the total)
     chunk = last;
     r = HUGE_VAL;
   }
-  // the first token whose end passes r, or the last of any weight
-  const E* const pr = target + s.x * p.target_stride;
-  const E* const qr = draft && s.A > 0.0 ? draft + s.x * p.draft_stride : nullptr;
-  int token = -1, tail = 0;
+  int tail = 0;
   before = found;
-  for (int j = 0; j < kPer / 8 && token < 0; ++j) {
+  for (int j = 0; j < kPer / 8; ++j) {
     const int v0 = chunk * kVerifyChunk + j * 512 + lane * 8;
     double w[8];
-    weights(p, s, pr, qr, s.A, s.ngone, v0, w);
+    weights(row, v0, w);
     double t = 0.0;
     int high = -1;
 #pragma unroll
@@ -270,37 +266,162 @@ __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyParams p) {
       if (w[i] > 0.0) high = i;
     }
     const double upto = before + wave_scan(t, lane);
-    double from = __shfl_up(upto, 1);
-    if (lane == 0) from = before;
+    double e = __shfl_up(upto, 1);
+    if (lane == 0) e = before;
     int mine = -1;
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-      // sums from the left
-      double e = from;
-#pragma unroll
-      for (int k = 0; k <= i; ++k) e += w[k];
-      if (e > r && w[i] > 0.0) mine = i;
+    for (int i = 0; i < 8; ++i) {
+      e += w[i];
+      if (mine < 0 && e > r && w[i] > 0.0) mine = i;
     }
     const uint64_t over = __ballot(mine >= 0), any = __ballot(high >= 0);
     if (over) {
       const int l = __builtin_ctzll(over);
-      token = chunk * kVerifyChunk + j * 512 + l * 8 + __builtin_amdgcn_readlane(mine, l);
-    } else if (any) {
+      return chunk * kVerifyChunk + j * 512 + l * 8 + __builtin_amdgcn_readlane(mine, l);
+    }
+    if (any) {
       const int l = 63 - __builtin_clzll(any);
       tail = chunk * kVerifyChunk + j * 512 + l * 8 + __builtin_amdgcn_readlane(high, l);
     }
     before = lane_double(upto, 63);
   }
-  if (lane == 0) p.next[b] = token >= 0 ? token : tail;
+  return tail;
+}
+
+template <typename E>
+__device__ inline const E* target_of(const VerifyParams& p, int b) { return (const E*)p.target + (int64_t)b * p.T * p.target_stride; }
+template <typename E>
+__device__ inline const E* draft_of(const VerifyParams& p, int b) {
+  return p.draft ? (const E*)p.draft + (int64_t)b * p.T * p.draft_stride : nullptr;
+}
+template <typename E>
+__device__ inline Row<E> row_of(const VerifyParams& p, int b, const Walk& w, const int32_t* gone) {
+  const E* const draft = draft_of<E>(p, b);
+  return {target_of<E>(p, b) + w.x * p.target_stride, draft && w.A > 0.0 ? draft + w.x * p.draft_stride : nullptr, w.A, gone, w.ngone, p.V};
+}
+
+// The results from the walk's end.  total: of the row as it is left, chunk by chunk in sums.
+template <typename E>
+__device__ inline void finish(const VerifyParams& p, int b, const Walk& w, const int32_t* path, Row<E> row, double* sums, double total) {
+  const int tid = threadIdx.x;
+  for (int i = tid; i < p.T; i += blockDim.x) p.nodes[(int64_t)b * p.T + i] = i < w.length ? path[i] : -1;
+  if (tid == 0) p.counts[b] = w.length;
+  if (total == 0.0 && (row.q || row.ngone > 0)) {      // nothing is left: the row itself
+    row.q = nullptr;
+    row.ngone = 0;
+    __syncthreads();
+    total = row_sums(p, row, sums);
+  }
+  if (tid >= 64) return;
+  const int token = total > 0.0 ? token_at(p, row, sums, uniform(p.uniforms[(int64_t)b * p.T]), total, tid) : -1;
+  if (tid == 0) p.next[b] = token;
+}
+
+// The walk from where it stands to its end, and the results.  One workgroup.  total: of the row that the walk waits for.
+template <typename E, int NODES>
+__device__ inline void go_on(const VerifyParams& p, Shared<NODES>& s, int b, int len, double* sums, double total) {
+  const int tid = threadIdx.x;
+  for (;;) {
+    // (the walk stops for the sum of a row of which A > 0, and ends there or at a row of which A = 0)
+    const bool waited = s.w.sum;
+    __syncthreads();
+    if (waited && !s.w.more) break;
+    if (tid == 0 && waited) s.w.W = total;
+    __syncthreads();
+    if (tid < 64) walk(s, len, p.draft != nullptr, tid);
+    __syncthreads();
+    if (!s.w.sum && waited && s.w.A > 0.0) break;      // refused no more: the sums stand
+    total = row_sums(p, row_of<E>(p, b, s.w, s.gone), sums);
+    if (!s.w.sum) break;
+  }
+  finish(p, b, s.w, s.path, row_of<E>(p, b, s.w, s.gone), sums, total);
+}
+
+__device__ inline bool nothing_to_do(const VerifyParams& p, int b) {
+  if (!p.draft_lens || p.draft_lens[b] > 0) return false;
+  for (int i = threadIdx.x; i < p.T; i += blockDim.x) p.nodes[(int64_t)b * p.T + i] = -1;
+  if (threadIdx.x == 0) {
+    p.counts[b] = 0;
+    p.next[b] = -1;
+  }
+  return true;
+}
+
+template <typename E, int NODES>
+__global__ __launch_bounds__(kThreads) void verify_kernel(VerifyParams p) {
+  __shared__ Shared<NODES> s;
+  const int b = blockIdx.x;
+  if (nothing_to_do(p, b)) return;
+  const int len = begin(p, s, b, target_of<E>(p, b), draft_of<E>(p, b));
+  go_on<E>(p, s, b, len, p.chunks <= kLdsChunks ? s.sums : scratch_of(p, b).sums, 0.0);
+}
+
+// In two kernels: the walk to the first row that is summed, and that row's sums ...
+constexpr int kSumThreads = 256;
+
+template <typename E, int NODES>
+__global__ __launch_bounds__(kSumThreads) void sums_kernel(VerifyParams p) {
+  __shared__ Shared<NODES> s;
+  const int b = blockIdx.y, tid = threadIdx.x;
+  if (p.draft_lens && p.draft_lens[b] <= 0) return;
+  const int len = begin(p, s, b, target_of<E>(p, b), draft_of<E>(p, b));
+  if (tid < 64) walk(s, len, p.draft != nullptr, tid);
+  __syncthreads();
+  const Scratch to = scratch_of(p, b);
+  const Row<E> row = row_of<E>(p, b, s.w, s.gone);
+  const int waves = gridDim.x * (kSumThreads / 64);
+  for (int i = blockIdx.x * (kSumThreads / 64) + tid / 64; i < p.chunks; i += waves) {
+    const double t = chunk_sum(row, i, tid & 63);
+    if ((tid & 63) == 0) to.sums[i] = t;
+  }
+  if (blockIdx.x > 0) return;
+  for (int i = tid; i < s.w.length; i += kSumThreads) to.path[i] = s.path[i];
+  for (int i = tid; i < s.w.ngone; i += kSumThreads) to.gone[i] = s.gone[i];
+  if (tid == 0) *to.w = s.w;
+}
+
+// ... and the results, or the rest of the walk where more than one row is summed.
+template <typename E, int NODES>
+__global__ __launch_bounds__(kThreads) void finish_kernel(VerifyParams p) {
+  __shared__ Shared<NODES> s;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  if (nothing_to_do(p, b)) return;
+  const Scratch from = scratch_of(p, b);
+  const Walk w = *from.w;
+  const double total = total_of(from.sums, p.chunks, tid & 63);
+  if (!w.more) {
+    finish(p, b, w, from.path, row_of<E>(p, b, w, from.gone), from.sums, total);
+    return;
+  }
+  const int len = begin(p, s, b, target_of<E>(p, b), draft_of<E>(p, b));
+  for (int i = tid; i < w.length; i += kThreads) s.path[i] = from.path[i];
+  if (tid == 0) s.w = w;
+  __syncthreads();
+  go_on<E>(p, s, b, len, from.sums, total);
+}
+
+template <typename E, int NODES>
+void launch(const VerifyParams& p, hipStream_t s) {
+  // Workgroups a sequence, so that about four a compute unit read the rows.
+  const int slices = std::min(1024 / p.B, (p.chunks + kSumThreads / 64 - 1) / (kSumThreads / 64));
+  if (p.chunks <= kWaves || slices < 2) {
+    verify_kernel<E, NODES><<<p.B, kThreads, 0, s>>>(p);
+    return;
+  }
+  sums_kernel<E, NODES><<<dim3((unsigned)slices, (unsigned)p.B), kSumThreads, 0, s>>>(p);
+  finish_kernel<E, NODES><<<p.B, kThreads, 0, s>>>(p);
 }
 
 }  // namespace
 
 hipError_t launch_draft_verify(const VerifyParams& p, int prob_bf16, hipStream_t stream) {
-  if (prob_bf16)
-    verify_kernel<uint16_t><<<p.B, kThreads, 0, stream>>>(p);
-  else
-    verify_kernel<float><<<p.B, kThreads, 0, stream>>>(p);
+  if (p.T <= 64) {
+    if (prob_bf16) launch<uint16_t, 64>(p, stream);
+    else launch<float, 64>(p, stream);
+  } else {
+    if (prob_bf16) launch<uint16_t, kMaxNodes>(p, stream);
+    else launch<float, kMaxNodes>(p, stream);
+  }
   return hipGetLastError();
 }
 
