@@ -23,6 +23,7 @@
 
 #include "pace_draft_internal.h"
 #include "pace_draft_tokens.h"
+#include "pace_lanes.h"
 
 namespace pace {
 namespace {
@@ -45,18 +46,18 @@ struct alignas(16) Smem {
   static constexpr int NK = 16 * NKT;
   static constexpr int TS = D + 8;              // row stride of tokens (bf16): 16 rows on distinct banks
   alignas(16) uint16_t k[NK][TS];               // key codes
-  alignas(16) uint16_t q[16 * PIECES][TS];      // one tile of queries
+  alignas(16) uint16_t q[16 * PIECES][TS];      // queries of one tile of tokens
   alignas(16) float u[NK][D];                   // v^, then u
-  struct Gram {
-    alignas(16) float a[NK][NK];                // [j][i]: beta_i D_ij (k_j . k_i), 0 for j >= i
-    alignas(16) float c[NK][16];                // [j][i]: D_ij (k_j . q_i) of one tile of queries
+  struct Gram {                                 // of one tile of tokens i and those before them
+    alignas(16) float a[NK][16];                // [j][i]: beta_i D_ij (k_j . k_i), 0 for j >= i
+    alignas(16) float c[NK][16];                // [j][i]: D_ij (k_j . q_i)
   };
   struct Scales {                               // of (32 keys, column), bf16
     alignas(16) uint16_t s[D / 32][D];
     alignas(16) uint16_t z[D / 32][D];          // minus what the operand's codes are too large by
   };
-  // One tile of tokens is projected before its Gram products are formed, so both fit one place (eight workgroups a
-  // compute unit at D = 128); with more tiles the scales are needed to the end.
+  // A tile is projected before its Gram products are formed, so both fit one place where there is one tile (eight
+  // workgroups a compute unit at D = 128); with more the scales are needed to the end.
   struct Both {
     Gram g;
     Scales s;
@@ -66,7 +67,7 @@ struct alignas(16) Smem {
     Scales s;
   };
   alignas(16) std::conditional_t<NKT == 1, Either, Both> m;
-  alignas(16) float ks[NK], decay[NK], beta[NK], gamma[NK];
+  alignas(16) float ks[NK], decay[NK], beta[NK], gamma[16];
   uint64_t row[NK < kMaxDrafts ? NK : kMaxDrafts];   // tree bits
 };
 
@@ -84,12 +85,8 @@ __device__ inline uint4 in_order(const float (&x)[8]) {
   return make_uint4(two_bf16(x[0], x[2]), two_bf16(x[1], x[3]), two_bf16(x[4], x[6]), two_bf16(x[5], x[7]));
 }
 
-__device__ inline float lane_value(float x, int lane) {
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
-}
-
 template <int D, int NKT, bool BF16, bool MIXED, bool BFS>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS && NKT == 1 ? 3 : 1)))
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS ? 3 : 1)))
 void step_kernel(DraftParams p) {
   constexpr int PIECES = BF16 ? 1 : 3;
   using SM = Smem<D, NKT, PIECES>;
@@ -156,17 +153,18 @@ void step_kernel(DraftParams p) {
       s.beta[e] = l.beta[tok * l.Hv + h];
     }
   };
-  auto load_queries = [&](int g, Raw8<BF16> (&x)[PASS]) {
+  // (queries of drafts first + 0 .. 15)
+  auto load_queries = [&](int first, Raw8<BF16> (&x)[PASS]) {
 #pragma unroll
     for (int e = 0; e < PASS; ++e)
-      x[e].load(l.q, (int64_t)(((tok0 + min(16 * g + ROWS * e + row0, T - 1)) * l.Hk + kh) * D + e0));
+      x[e].load(l.q, (int64_t)(((tok0 + min(max(first + ROWS * e + row0, 0), T - 1)) * l.Hk + kh) * D + e0));
   };
   Slots slots;
   load_slots(0, slots);
   Drafts drafts;
   load_drafts(0, drafts);
   Raw8<BF16> queries[PASS];
-  load_queries(0, queries);
+  if constexpr (NKT == 1) load_queries(0, queries);
   uint64_t bitsrow = ~0ull;
   if (p.tree) {
     const int words = (T + 31) / 32;
@@ -223,7 +221,8 @@ void step_kernel(DraftParams p) {
   }
 
   // ----------------------------------------------------------------- tokens
-  const int len = min(max(len_raw, 0), T), n = min(max(count, 0), l.dP - 1), N = n + len;
+  const int len = __builtin_amdgcn_readfirstlane(min(max(len_raw, 0), T));
+  const int n = __builtin_amdgcn_readfirstlane(min(max(count, 0), l.dP - 1)), N = n + len;
   const int NT = (N + 15) / 16, NR = 16 * NT;        // tiles and rows in use
   auto store_rows = [&](int t, const float (&x)[SPW]) {
     const size_t at = ((tok0 + t) * l.Hv + h) * D + c0;
@@ -300,14 +299,14 @@ void step_kernel(DraftParams p) {
       if (t < len) put(n + t, kx, vx, ks, s.a[e], s.beta[e]);
     }
   };
-  auto take_queries = [&](int g, const Raw8<BF16> (&in)[PASS]) {
+  // into rows row + 0 .. 15 of the tile, as far as they are in it
+  auto take_queries = [&](int row, const Raw8<BF16> (&in)[PASS]) {
 #pragma unroll
     for (int e = 0; e < PASS; ++e) {
-      const int i = ROWS * e + row0;
+      const int i = row + ROWS * e + row0;
+      if (i < 0 || i >= 16) continue;
       float x[8];
       in[e].values(x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 16 * g + i < len ? x[j] : 0.f;
 #pragma unroll
       for (int c = 0; c < PIECES; ++c) {
         *(uint4*)&sm.q[16 * c + i][e0] = in_order<BFS>(x);
@@ -324,8 +323,11 @@ void step_kernel(DraftParams p) {
   };
   take_slots(0, slots);
   take_drafts(0, drafts);
-  take_queries(0, queries);
-  if constexpr (NKT > 1) {
+  if constexpr (NKT == 1) {
+    take_queries(n, queries);                          // (every token is in the one tile)
+  } else {
+    load_queries(-n, queries);
+    take_queries(0, queries);
     for (int g = 1; 16 * g < n; ++g) {
       load_slots(g, slots);
       take_slots(g, slots);
@@ -354,139 +356,148 @@ void step_kernel(DraftParams p) {
   }
   __syncthreads();
 
-  // ------------------------------------------------------------- projections
   auto operand = [&](const uint16_t* row) { return *(const v8bf*)(row + 8 * qq); };
-  // Of 16 tokens (P operands for every 32 keys) on the wave's columns: x[s] of strip s, tokens 4 qq + r.
-  auto project = [&](auto pieces, auto eight_bits, const uint16_t* rows, v4f (&x)[SPW]) {
-    constexpr int P = decltype(pieces)::value;
+  // Projections of a tile's keys and queries on the wave's columns: [s] of strip s, tokens 4 qq + r.  Two strips and 32 keys
+  // at a time: all at once, the operands and sums are some 100 registers more.
+  auto project = [&](auto eight_bits, const uint16_t* rows, v4f (&xk)[SPW], v4f (&xq)[SPW]) {
     constexpr bool E8 = decltype(eight_bits)::value;
+    constexpr v4f none = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < SPW; ++s) x[s] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < SPW; ++s) xk[s] = xq[s] = none;
+    v4f ak[2][2], aq[2][2];                    // [turn][strip of the pair]
+    uint32_t sc[2];
+    // one turn's sums, scaled: while the next turn's products are formed
+    auto add = [&](int turn) {
+      const int s0 = 2 * (turn / KB);
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      v8bf tok[P];
+      for (int s = 0; s < 2; ++s) {
+        const float scale = bits_f32(s ? sc[turn & 1] & 0xFFFF0000u : sc[turn & 1] << 16);
 #pragma unroll
-      for (int e = 0; e < P; ++e) tok[e] = operand(rows + (size_t)(16 * e + l16) * SM::TS + 32 * kb);
+        for (int r = 0; r < 4; ++r) {
+          xk[s0 + s][r] = fmaf(scale, ak[turn & 1][s][r], xk[s0 + s][r]);
+          xq[s0 + s][r] = fmaf(scale, aq[turn & 1][s][r], xq[s0 + s][r]);
+        }
+        asm volatile("" : "+v"(xk[s0 + s]), "+v"(xq[s0 + s]));
+      }
+    };
+#pragma unroll
+    for (int turn = 0; turn < SPW / 2 * KB; ++turn) {
+      const int s0 = 2 * (turn / KB), kb = turn % KB;
+      // (a turn's operands are not begun before it: they depend on these)
+      int own = l16;
+      asm volatile("" : "+v"(own));
+      if constexpr (!BFS)
+#pragma unroll
+        for (int s = s0; s < s0 + 2; ++s)
+#pragma unroll
+          for (int i = 0; i < (E8 ? 2 : 1); ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb + i : kb]));
+      const v8bf tk = operand(rows + (size_t)own * SM::TS + 32 * kb);
+      v8bf tq[PIECES];
+#pragma unroll
+      for (int e = 0; e < PIECES; ++e) tq[e] = operand(&sm.q[16 * e + own][32 * kb]);
+      auto queries_times = [&](v8bf x, v4f acc) {
+#pragma unroll
+        for (int e = 0; e < PIECES; ++e) acc = mfma(tq[e], x, acc);
+        return acc;
+      };
       if constexpr (BFS) {
 #pragma unroll
-        for (int s = 0; s < SPW; ++s)
-#pragma unroll
-          for (int e = 0; e < P; ++e)
-            x[s] = mfma(tok[e], as_operand(raw[s][4 * kb], raw[s][4 * kb + 1], raw[s][4 * kb + 2], raw[s][4 * kb + 3]), x[s]);
+        for (int s = s0; s < s0 + 2; ++s) {
+          const v8bf st = as_operand(raw[s][4 * kb], raw[s][4 * kb + 1], raw[s][4 * kb + 2], raw[s][4 * kb + 3]);
+          xk[s] = mfma(tk, st, xk[s]);
+          xq[s] = queries_times(st, xq[s]);
+        }
         continue;
       }
-      uint32_t sc[SPW / 2], zp[SPW / 2];       // of the lane's columns
+      v4f (&k)[2] = ak[turn & 1], (&q)[2] = aq[turn & 1];
+      sc[turn & 1] = *(const uint32_t*)&sm.m.s.s[kb][c0 + s0];
+      if (asym) {
+        const uint32_t zp = *(const uint32_t*)&sm.m.s.z[kb][c0 + s0];
 #pragma unroll
-      for (int s = 0; s < SPW / 2; ++s) {
-        sc[s] = *(const uint32_t*)&sm.m.s.s[kb][c0 + 2 * s];
-        zp[s] = *(const uint32_t*)&sm.m.s.z[kb][c0 + 2 * s];
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t z = __builtin_amdgcn_perm(zp, zp, s ? 0x03020302u : 0x01000100u);
+          k[s] = mfma(tk, as_operand(z, z, z, z), none);
+          q[s] = queries_times(as_operand(z, z, z, z), none);
+        }
+      } else {                                 // symmetric: the same offset for every column, -24 or -128
+        const uint32_t z = E8 ? 0xC300C300u : 0xC1C0C1C0u;
+        k[0] = k[1] = mfma(tk, as_operand(z, z, z, z), none);
+        q[0] = q[1] = queries_times(as_operand(z, z, z, z), none);
       }
 #pragma unroll
-      for (int s = 0; s < SPW; ++s) {
-        // (unpacked where they are used: kept from one use to the next, the operands of a tile are 64 registers)
-#pragma unroll
-        for (int i = 0; i < (E8 ? 2 : 1); ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb + i : kb]));
+      for (int s = 0; s < 2; ++s) {
         v8bf st;
         if constexpr (E8) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t y = raw[s][2 * kb + e];
+            const uint32_t y = raw[s0 + s][2 * kb + e];
             w[2 * e] = two_bf16((float)(y & 255u), (float)((y >> 16) & 255u));
             w[2 * e + 1] = two_bf16((float)((y >> 8) & 255u), (float)(y >> 24));
           }
           st = as_operand(w[0], w[1], w[2], w[3]);
         } else {
-          const uint32_t y = raw[s][kb];
+          const uint32_t y = raw[s0 + s][kb];
           st = as_operand(((y << 3) & 0x00780078u) | 0x41804180u, ((y >> 5) & 0x00780078u) | 0x41804180u,
                           ((y >> 1) & 0x00780078u) | 0x41804180u, ((y >> 9) & 0x00780078u) | 0x41804180u);
         }
-        const uint32_t z = __builtin_amdgcn_perm(zp[s / 2], zp[s / 2], s & 1 ? 0x03020302u : 0x01000100u);
-        v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < P; ++e) acc = mfma(tok[e], as_operand(z, z, z, z), acc);
-#pragma unroll
-        for (int e = 0; e < P; ++e) acc = mfma(tok[e], st, acc);
-        const float scale = bits_f32(s & 1 ? sc[s / 2] & 0xFFFF0000u : sc[s / 2] << 16);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[s][r] = fmaf(scale, acc[r], x[s][r]);
+        k[s] = mfma(tk, st, k[s]);
+        q[s] = queries_times(st, q[s]);
       }
+      if (turn > 0) add(turn - 1);
     }
+    if constexpr (!BFS) add(SPW / 2 * KB - 1);
   };
-  auto project_any = [&](auto pieces, const uint16_t* rows, v4f (&x)[SPW]) {
-    if (is8) project(pieces, std::true_type{}, rows, x);
-    else project(pieces, std::false_type{}, rows, x);
-  };
-  v4f xq[SPW], xk[SPW];
-  project_any(std::integral_constant<int, PIECES>{}, &sm.q[0][0], xq);
-  project_any(std::integral_constant<int, 1>{}, &sm.k[0][0], xk);
-  if constexpr (NKT == 1) __syncthreads();     // the scales have been read: the Gram products take their place
-
-  // --------------------------------------------------------- decays and Gram
-  // The products of row i, walked back from its own token by one lane: at[j * stride] = D_ij where j is on its path, else 0.
-  // own: its own token is among them (with 1).  Returns the product of them all.
-  const float decay0 = sm.decay[min(lane, NR - 1)], decay1 = NKT > 4 ? sm.decay[min(64 + lane, NR - 1)] : 0.f;
-  auto walk_back = [&](int i, bool own, float* at, int stride, bool in) {
-    const uint64_t on_path = i >= n && i < N ? sm.row[i - n] : ~0ull;
-    const uint32_t lo = (uint32_t)on_path, hi = (uint32_t)(on_path >> 32);
-    in = in && i < N;
-    float prod = own ? 1.f : sm.decay[min(i, NR - 1)];
-    for (int j = NR - 1; j >= 0; --j) {
-      const float dj = NKT > 4 && j >= 64 ? lane_value(decay1, j - 64) : lane_value(decay0, j);
-      const uint32_t word = j - n >= 32 ? hi : lo;
-      const bool on = in && ((own && j == i) || (j < i && (j < n || ((word >> ((j - n) & 31)) & 1u))));
-      at[j * stride] = on ? prod : 0.f;
-      prod = on ? prod * dj : prod;
-    }
-    return prod;
-  };
-  // a[j][i] of one tile of i and one of j (jt <= it)
-  auto gram_keys = [&](int it, int jt) {
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
+  // The decays and Gram products of a tile with the tokens before it, in the matrix unit's layout: token i = 16 t + l16 a lane,
+  // tokens j 4 qq + r of 16 jt.  From the tile's own end back to the first token: D_ij is the product of the decays on i's path
+  // behind j, i's own among them: those behind in the lane's four, in the rows of lanes above, and in the tiles behind.
+  auto gram = [&](auto of_queries, int t) {
+    constexpr bool Q = decltype(of_queries)::value;
+    const int i = 16 * t + l16;
+    const uint64_t path = i >= n && i < N ? sm.row[i - n] : ~0ull;
+    const uint32_t lo = (uint32_t)path, hi = (uint32_t)(path >> 32);
+    // bit j of the three words: token j is on i's path (buffered ones are)
+    const uint32_t w0 = n ? lo << n | ((1u << n) - 1u) : lo, w1 = n ? hi << n | lo >> (32 - n) : hi, w2 = n ? hi >> (32 - n) : 0u;
+    const uint32_t v0 = i < n ? ~0u : w0, v1 = i < n ? ~0u : w1, v2 = i < n ? ~0u : w2;
+    const float own = Q ? 1.f : sm.beta[i] * sm.ks[i];
+    float behind = 1.f;
+    for (int jt = t; jt >= 0; --jt) {
+      v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) acc = mfma(operand(&sm.k[16 * it + l16][32 * kb]), operand(&sm.k[16 * jt + l16][32 * kb]), acc);
-    const int j = 16 * jt + l16, i = 16 * it + 4 * qq;
-    float4* at = (float4*)&sm.m.g.a[j][i];
-    const float4 d = *at, ksi = *(const float4*)&sm.ks[i], be = *(const float4*)&sm.beta[i];
-    const float kj = sm.ks[j];
-    *at = make_float4(d.x * be.x * ksi.x * kj * acc[0], d.y * be.y * ksi.y * kj * acc[1], d.z * be.z * ksi.z * kj * acc[2],
-                      d.w * be.w * ksi.w * kj * acc[3]);
-  };
-  // c[j][i] of the tile of queries and one of j
-  auto gram_queries = [&](int jt) {
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
+      for (int kb = 0; kb < KB; ++kb) {
+        const v8bf kj = operand(&sm.k[16 * jt + l16][32 * kb]);
+        if constexpr (Q) {
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+          for (int e = 0; e < PIECES; ++e) acc = mfma(kj, operand(&sm.q[16 * e + l16][32 * kb]), acc);
+        } else {
+          acc = mfma(kj, operand(&sm.k[16 * t + l16][32 * kb]), acc);
+        }
+      }
+      const int j = 16 * jt + 4 * qq;
+      const uint32_t nibble = (jt < 2 ? v0 : jt < 4 ? v1 : v2) >> (16 * (jt & 1) + 4 * qq);
+      const float4 dj = *(const float4*)&sm.decay[j], kj = *(const float4*)&sm.ks[j];
+      const float d[4] = {dj.x, dj.y, dj.z, dj.w}, ks[4] = {kj.x, kj.y, kj.z, kj.w};
+      bool on[4];
+      float f[4];
 #pragma unroll
-      for (int e = 0; e < PIECES; ++e)
-        acc = mfma(operand(&sm.q[16 * e + l16][32 * kb]), operand(&sm.k[16 * jt + l16][32 * kb]), acc);
-    const int j = 16 * jt + l16;
-    float4* at = (float4*)&sm.m.g.c[j][4 * qq];
-    const float4 d = *at;
-    const float kj = sm.ks[j];
-    *at = make_float4(d.x * kj * acc[0], d.y * kj * acc[1], d.z * kj * acc[2], d.w * kj * acc[3]);
+      for (int r = 0; r < 4; ++r) {
+        on[r] = i < N && j + r < i && ((nibble >> r) & 1u);
+        f[r] = on[r] || j + r == i ? d[r] : 1.f;
+        if (Q) on[r] = on[r] || (i < N && j + r == i);
+      }
+      const float f32_ = f[3] * f[2], f321 = f32_ * f[1];
+      uint32_t rows[4];
+      rows_gather(f32_bits(f321 * f[0]), 4, rows);
+      const float g1 = bits_f32(rows[1]), g2 = bits_f32(rows[2]), g3 = bits_f32(rows[3]), g32_ = g3 * g2, g321 = g32_ * g1;
+      const float above = behind * (qq == 0 ? g321 : qq == 1 ? g32_ : qq == 2 ? g3 : 1.f);
+      const float p[4] = {f321, f32_, f[3], 1.f};
+      float (*to)[16] = Q ? sm.m.g.c : sm.m.g.a;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) to[j + r][l16] = on[r] ? above * p[r] * (own * ks[r]) * acc[r] : 0.f;
+      behind *= g321 * bits_f32(rows[0]);
+    }
+    if (!Q && qq == 0) sm.gamma[l16] = behind;
   };
-  if constexpr (NKT == 1) {
-    // one wave the keys', the other the queries'
-    if (wave == 0) {
-      if (lane < 16) sm.gamma[lane] = walk_back(lane, false, &sm.m.g.a[0][lane], SM::NK, true);
-      wave_sync();
-      gram_keys(0, 0);
-    } else {
-      if (lane < 16) walk_back(n + lane, true, &sm.m.g.c[0][lane], 16, lane < len);
-      wave_sync();
-      gram_queries(0);
-    }
-  } else {
-    for (int i0 = 64 * wave; i0 < NR; i0 += 64 * kWaves)
-      if (i0 + lane < NR) sm.gamma[i0 + lane] = walk_back(i0 + lane, false, &sm.m.g.a[0][i0 + lane], SM::NK, true);
-    __syncthreads();
-    for (int t = wave; t < NT * NT; t += kWaves) {
-      const int it = t / NT, jt = t % NT;
-      if (jt <= it) gram_keys(it, jt);
-    }
-  }
-
   auto columns = [&](const float* row, float (&y)[SPW]) {
     if constexpr (SPW == 4) {
       const float4 v = *(const float4*)(row + c0);
@@ -496,35 +507,45 @@ void step_kernel(DraftParams p) {
       y[0] = v.x; y[1] = v.y;
     }
   };
-  // x += what the tokens below `end` add, four an instruction (fp32): weights at[j * stride + l16], times sign
-  auto add_tokens = [&](int end, const float* at, int stride, float sign, v4f (&x)[SPW]) {
+  // x += what the tokens below `end` add, four an instruction (fp32): weights at[j][l16], times sign
+  auto add_tokens = [&](int end, const float (*at)[16], float sign, v4f (&x)[SPW]) {
     for (int j = qq; j < end + qq; j += 4) {
-      const float w = sign * at[j * stride + l16];
+      const float w = sign * at[j][l16];
       float u[SPW];
       columns(sm.u[j], u);
 #pragma unroll
       for (int s = 0; s < SPW; ++s) x[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, u[s], x[s], 0, 0, 0);
     }
   };
-  if constexpr (NKT > 1) {
-    // (the first tile of queries' decays; their Gram products wait for the barrier)
-    if (wave == 1 && lane < 16) walk_back(n + lane, true, &sm.m.g.c[0][lane], 16, lane < len);
-  }
-  __syncthreads();
 
-  // ------------------------------------------------------------------ solve
   for (int t = 0; t < NT; ++t) {
-    if (t > 0) project_any(std::integral_constant<int, 1>{}, &sm.k[16 * t][0], xk);
+    if constexpr (NKT > 1) {
+      if (t > 0) {
+        __syncthreads();                       // the tile before is done with its queries and products
+        load_queries(16 * t - n, queries);
+        take_queries(0, queries);
+        __syncthreads();
+      }
+    }
+    v4f xk[SPW], xq[SPW];
+    if (is8) project(std::true_type{}, &sm.k[16 * t][0], xk, xq);
+    else project(std::false_type{}, &sm.k[16 * t][0], xk, xq);
+    if constexpr (NKT == 1) __syncthreads();   // the scales have been read: the Gram products take their place
+    if (wave == 0) gram(std::false_type{}, t);
+    else gram(std::true_type{}, t);
+    __syncthreads();
+
+    // ---------------------------------------------------------------- solve
     const int i0 = 16 * t + 4 * qq;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float be = sm.beta[i0 + r], f = be * sm.gamma[i0 + r] * sm.ks[i0 + r];
+      const float be = sm.beta[i0 + r], f = be * sm.gamma[4 * qq + r] * sm.ks[i0 + r];
       float v[SPW];
       columns(sm.u[i0 + r], v);
 #pragma unroll
       for (int s = 0; s < SPW; ++s) xk[s][r] = be * v[s] - f * xk[s][r];
     }
-    if (t > 0) add_tokens(16 * t, &sm.m.g.a[0][16 * t], SM::NK, -1.f, xk);
+    if (NKT > 1 && t > 0) add_tokens(16 * t, sm.m.g.a, -1.f, xk);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float* row = &sm.u[i0 + r][c0];
@@ -539,7 +560,7 @@ void step_kernel(DraftParams p) {
       for (int i = 0; i < 16; ++i) y[i] = sm.u[16 * t + i][c];
 #pragma unroll
       for (int j = 0; j < 15; ++j) {
-        const float* a = &sm.m.g.a[16 * t + j][16 * t];
+        const float* a = sm.m.g.a[16 * t + j];
 #pragma unroll
         for (int i = j + 1; i < 16; ++i) y[i] -= a[i] * y[j];
       }
@@ -547,38 +568,22 @@ void step_kernel(DraftParams p) {
       for (int i = 1; i < 16; ++i) sm.u[16 * t + i][c] = y[i];
     }
     wave_sync();
-  }
 
-  // ---------------------------------------------------------------- outputs
-  for (int t0 = 0; t0 < len; t0 += 16) {
-    const int end = min(N, n + t0 + 16);
-    if constexpr (NKT > 1) {
-      if (t0 > 0) {
-        __syncthreads();
-        load_queries(t0 / 16, queries);
-        take_queries(t0 / 16, queries);
-        if (wave == 1 && lane < 16) walk_back(n + t0 + lane, true, &sm.m.g.c[0][lane], 16, t0 + lane < len);
-        __syncthreads();
-        project_any(std::integral_constant<int, PIECES>{}, &sm.q[0][0], xq);
-      }
-      for (int jt = wave; 16 * jt < end; jt += kWaves) gram_queries(jt);
-      __syncthreads();
-    }
+    // -------------------------------------------------------------- outputs
+    if (16 * t + 16 <= n) continue;            // buffered tokens only
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int t = t0 + 4 * qq + r;
-      const float g = t < len ? sm.gamma[n + t] : 0.f;
+      const float g = sm.gamma[4 * qq + r];
 #pragma unroll
       for (int s = 0; s < SPW; ++s) xq[s][r] *= g;
     }
-    add_tokens(end, &sm.m.g.c[0][0], 16, 1.f, xq);
+    add_tokens(min(N, 16 * t + 16), sm.m.g.c, 1.f, xq);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int t = t0 + 4 * qq + r;
       float y[SPW];
 #pragma unroll
       for (int s = 0; s < SPW; ++s) y[s] = xq[s][r];
-      if (t < len) store_rows(t, y);
+      if (i0 + r >= n && i0 + r < N) store_rows(i0 + r - n, y);
     }
   }
 }
