@@ -11,11 +11,9 @@
 //   decays       row i's products by one lane, walking its path back
 //   Gram         k_j . k_i and k_j . q_i on the bf16 matrix cores, times the decays
 //   projections  tokens (A) times state columns (B), 32 keys an instruction.  A 4-bit code c becomes the bf16 number 16 + c by
-//                a shift and a mask-and-or of two codes; a second product with -(16 + z) takes the offset and the zero
-//                point off, so that the sums are exact for key codes.  One scale a (column, group).
-//   solve        16 tokens at a time: what the tokens before them add in the matrix unit's layout (4 tokens x 4 columns
-//                a lane), then the 16 x 16 triangle, one column a lane
-//   outputs      16 queries at a time, the same way
+//                a shift and a mask-and-or of two codes; the offset and the zero point are taken off by the tokens' block
+//                sums.  One scale a (column, 32 keys).
+//   solve        16 tokens at a time in the matrix unit's layout (4 tokens x 4 columns a lane), four at a time within them
 // Queries enter as they are in bf16, as three bf16 pieces (exact) in fp32.  Everything else is fp32.
 #include <hip/hip_runtime.h>
 
@@ -85,8 +83,9 @@ __device__ inline uint4 in_order(const float (&x)[8]) {
   return make_uint4(two_bf16(x[0], x[2]), two_bf16(x[1], x[3]), two_bf16(x[4], x[6]), two_bf16(x[5], x[7]));
 }
 
-template <int D, int NKT, bool BF16, bool MIXED, bool BFS>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS ? 3 : 1)))
+// HB: 4 = every head 4-bit, 0 = by the head map.
+template <int D, int NKT, bool BF16, bool MIXED, int HB, bool BFS>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS ? (HB == 4 && NKT == 1 ? 4 : 3) : 1)))
 void step_kernel(DraftParams p) {
   constexpr int PIECES = BF16 ? 1 : 3;
   using SM = Smem<D, NKT, PIECES>;
@@ -119,45 +118,63 @@ void step_kernel(DraftParams p) {
     uint32_t k[PASS][2], v[PASS][MIXED ? 4 : 2];
     float ks[PASS], vs[PASS], a[PASS], beta[PASS];
   };
+  // (bases are the workgroup's: scalar registers; lanes add 32 bits)
+  const size_t kslot0 = ((size_t)b * l.Hk + kh) * l.dP, vslot0 = bh * l.dP;
+  const uint8_t* const buf_k = l.buffer + l.off_kc + kslot0 * (MIXED ? D / 2 : D);
+  const uint8_t* const buf_v = l.buffer + l.off_v + vslot0 * (MIXED ? 2 * D : D);
+  const float* const buf_ks = (const float*)(l.buffer + l.off_ks) + kslot0;
+  const float* const buf_vs = (const float*)(l.buffer + l.off_vs) + vslot0;
+  const float* const buf_a = (const float*)(l.buffer + l.off_a) + vslot0;
+  const float* const buf_beta = (const float*)(l.buffer + l.off_beta) + vslot0;
   auto load_slots = [&](int g, Slots& s) {
 #pragma unroll
     for (int e = 0; e < PASS; ++e) {
-      const int i = min(16 * g + ROWS * e + row0, l.dP - 1);
-      const size_t kslot = ((size_t)b * l.Hk + kh) * l.dP + i, vslot = bh * l.dP + i;
+      if (16 * g + ROWS * e >= l.dP - 1) continue;       // (at most dP - 1 are held)
+      const uint32_t i = min(16 * g + ROWS * e + row0, l.dP - 1);
       if constexpr (MIXED) {
-        s.k[e][0] = *(const uint32_t*)(l.buffer + l.off_kc + kslot * (D / 2) + e0 / 2);
-        const uint4 w = *(const uint4*)(l.buffer + l.off_v + (vslot * D + e0) * 2);
+        s.k[e][0] = *(const uint32_t*)(buf_k + (i * (D / 2) + e0 / 2));
+        const uint4 w = *(const uint4*)(buf_v + (i * D + e0) * 2);
         s.v[e][0] = w.x; s.v[e][1] = w.y; s.v[e][2] = w.z; s.v[e][3] = w.w;
       } else {
-        const uint2 w = *(const uint2*)(l.buffer + l.off_kc + kslot * D + e0), x = *(const uint2*)(l.buffer + l.off_v + vslot * D + e0);
+        const uint2 w = *(const uint2*)(buf_k + (i * D + e0)), x = *(const uint2*)(buf_v + (i * D + e0));
         s.k[e][0] = w.x; s.k[e][1] = w.y;
         s.v[e][0] = x.x; s.v[e][1] = x.y;
-        s.vs[e] = ((const float*)(l.buffer + l.off_vs))[vslot];
+        s.vs[e] = buf_vs[i];
       }
-      s.ks[e] = ((const float*)(l.buffer + l.off_ks))[kslot];
-      s.a[e] = ((const float*)(l.buffer + l.off_a))[vslot];
-      s.beta[e] = ((const float*)(l.buffer + l.off_beta))[vslot];
+      s.ks[e] = buf_ks[i];
+      s.a[e] = buf_a[i];
+      s.beta[e] = buf_beta[i];
     }
   };
   struct Drafts {
     Raw8<BF16> k[PASS], v[PASS];
     float a[PASS], beta[PASS];
   };
+  constexpr int E = BF16 ? 2 : 4;
+  const uint8_t* const in_k = (const uint8_t*)l.k + (tok0 * l.Hk + kh) * D * E;
+  const uint8_t* const in_q = (const uint8_t*)l.q + (tok0 * l.Hk + kh) * D * E;
+  const uint8_t* const in_v = (const uint8_t*)l.v + (tok0 * l.Hv + h) * D * E;
+  const float* const in_a = l.a + tok0 * l.Hv + h;
+  const float* const in_beta = l.beta + tok0 * l.Hv + h;
+  const uint32_t next_k = (uint32_t)l.Hk * D * E, next_v = (uint32_t)l.Hv * D * E;   // (of a token; T of them: under 2^22)
   auto load_drafts = [&](int g, Drafts& s) {
 #pragma unroll
     for (int e = 0; e < PASS; ++e) {
-      const size_t tok = tok0 + min(16 * g + ROWS * e + row0, T - 1);
-      s.k[e].load(l.k, (int64_t)((tok * l.Hk + kh) * D + e0));
-      s.v[e].load(l.v, (int64_t)((tok * l.Hv + h) * D + e0));
-      s.a[e] = l.a[tok * l.Hv + h];
-      s.beta[e] = l.beta[tok * l.Hv + h];
+      if (16 * g + ROWS * e >= T) continue;
+      const uint32_t t = min(16 * g + ROWS * e + row0, T - 1);
+      s.k[e].load(in_k + (t * next_k + e0 * E));
+      s.v[e].load(in_v + (t * next_v + e0 * E));
+      s.a[e] = in_a[t * (uint32_t)l.Hv];
+      s.beta[e] = in_beta[t * (uint32_t)l.Hv];
     }
   };
   // (queries of drafts first + 0 .. 15)
   auto load_queries = [&](int first, Raw8<BF16> (&x)[PASS]) {
 #pragma unroll
-    for (int e = 0; e < PASS; ++e)
-      x[e].load(l.q, (int64_t)(((tok0 + min(max(first + ROWS * e + row0, 0), T - 1)) * l.Hk + kh) * D + e0));
+    for (int e = 0; e < PASS; ++e) {
+      if (first + ROWS * e >= T) continue;
+      x[e].load(in_q + ((uint32_t)min(max(first + ROWS * e + row0, 0), T - 1) * next_k + e0 * E));
+    }
   };
   Slots slots;
   load_slots(0, slots);
@@ -173,17 +190,17 @@ void step_kernel(DraftParams p) {
   }
 
   // ------------------------------------------------------------------ state
-  const bool is8 = !BFS && ((l.mask8 >> h) & 1ull) != 0, asym = l.asym != 0;
+  const bool is8 = HB != 4 && !BFS && ((l.mask8 >> h) & 1ull) != 0, asym = l.asym != 0;
   const int bits = BFS ? 16 : is8 ? 8 : 4;
-  const uint64_t below = h ? (l.mask8 & ((1ull << h) - 1ull)) : 0ull;
+  const uint64_t below = HB != 4 && h ? (l.mask8 & ((1ull << h) - 1ull)) : 0ull;
   const uint8_t* rec = l.state + (uint64_t)b * l.seq_stride + (uint64_t)h * l.rec4 + (uint64_t)__popcll(below) * (l.rec8 - l.rec4);
   // a lane's columns: c0 .. c0 + SPW - 1, one a strip; their codes of keys 8 qq .. + 7 of every 32 (one unit each)
   const int c0 = wave * CW + SPW * l16;
-  constexpr int AW = BFS ? 4 * KB : 2 * KB;
+  constexpr int AW = BFS ? 4 * KB : HB == 4 ? KB : 2 * KB;
   uint32_t raw[SPW][AW];
 #pragma unroll
   for (int s = 0; s < SPW; ++s) {
-    const uint8_t* col = rec + (size_t)(c0 + s) * (D * bits / 8);
+    const uint8_t* col = rec + (uint32_t)((c0 + s) * (D * bits / 8));
     if constexpr (BFS) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
@@ -191,10 +208,12 @@ void step_kernel(DraftParams p) {
         raw[s][4 * kb] = v.x; raw[s][4 * kb + 1] = v.y; raw[s][4 * kb + 2] = v.z; raw[s][4 * kb + 3] = v.w;
       }
     } else if (is8) {
+      if constexpr (HB != 4) {
 #pragma unroll
-      for (int kb = 0; kb < KB; kb += 2) {
-        const uint4 v = *(const uint4*)(col + 8 * (qq * KB + kb));
-        raw[s][2 * kb] = v.x; raw[s][2 * kb + 1] = v.y; raw[s][2 * kb + 2] = v.z; raw[s][2 * kb + 3] = v.w;
+        for (int kb = 0; kb < KB; kb += 2) {
+          const uint4 v = *(const uint4*)(col + 8 * (qq * KB + kb));
+          raw[s][2 * kb] = v.x; raw[s][2 * kb + 1] = v.y; raw[s][2 * kb + 2] = v.z; raw[s][2 * kb + 3] = v.w;
+        }
       }
     } else if constexpr (KB == 4) {
       const uint4 v = *(const uint4*)(col + 16 * qq);
@@ -224,17 +243,18 @@ void step_kernel(DraftParams p) {
   const int len = __builtin_amdgcn_readfirstlane(min(max(len_raw, 0), T));
   const int n = __builtin_amdgcn_readfirstlane(min(max(count, 0), l.dP - 1)), N = n + len;
   const int NT = (N + 15) / 16, NR = 16 * NT;        // tiles and rows in use
+  uint8_t* const out = (uint8_t*)l.o + (tok0 * l.Hv + h) * D * E;
   auto store_rows = [&](int t, const float (&x)[SPW]) {
-    const size_t at = ((tok0 + t) * l.Hv + h) * D + c0;
+    uint8_t* const at = out + ((uint32_t)t * next_v + c0 * E);
     if constexpr (BF16) {
       uint32_t w[SPW / 2];
 #pragma unroll
       for (int s = 0; s < SPW / 2; ++s) w[s] = two_bf16(x[2 * s], x[2 * s + 1]);
-      if constexpr (SPW == 4) *(uint2*)((uint16_t*)l.o + at) = make_uint2(w[0], w[1]);
-      else *(uint32_t*)((uint16_t*)l.o + at) = w[0];
+      if constexpr (SPW == 4) *(uint2*)at = make_uint2(w[0], w[1]);
+      else *(uint32_t*)at = w[0];
     } else {
-      if constexpr (SPW == 4) *(float4*)((float*)l.o + at) = make_float4(x[0], x[1], x[2], x[3]);
-      else *(float2*)((float*)l.o + at) = make_float2(x[0], x[1]);
+      if constexpr (SPW == 4) *(float4*)at = make_float4(x[0], x[1], x[2], x[3]);
+      else *(float2*)at = make_float2(x[0], x[1]);
     }
   };
   if (len < T) {
@@ -256,7 +276,7 @@ void step_kernel(DraftParams p) {
 #pragma unroll
     for (int e = 0; e < PASS; ++e) {
       const int i = 16 * g + ROWS * e + row0;
-      if (i >= n) continue;
+      if (16 * g + ROWS * e >= n) continue;              // (of the workgroup: nothing is computed for nobody)
       float kx[8], vx[8];
       if constexpr (MIXED) {
 #pragma unroll
@@ -273,13 +293,14 @@ void step_kernel(DraftParams p) {
           vx[j] = (float)(int8_t)(s.v[e][j / 4] >> (8 * (j & 3))) * s.vs[e];
         }
       }
-      put(i, kx, vx, s.ks[e], s.a[e], s.beta[e]);
+      if (i < n) put(i, kx, vx, s.ks[e], s.a[e], s.beta[e]);
     }
   };
   auto take_drafts = [&](int g, const Drafts& s) {
 #pragma unroll
     for (int e = 0; e < PASS; ++e) {
       const int t = 16 * g + ROWS * e + row0;
+      if (16 * g + ROWS * e >= len) continue;
       float x[8], kx[8], vx[8];
       s.k[e].values(x);
       const float ks = quantise8<LANES>(x, MIXED, kx);
@@ -299,11 +320,12 @@ void step_kernel(DraftParams p) {
       if (t < len) put(n + t, kx, vx, ks, s.a[e], s.beta[e]);
     }
   };
-  // into rows row + 0 .. 15 of the tile, as far as they are in it
-  auto take_queries = [&](int row, const Raw8<BF16> (&in)[PASS]) {
+  // of drafts first + 0 .. 15 into rows row + 0 .. 15 of the tile, as far as they are in it
+  auto take_queries = [&](int first, int row, const Raw8<BF16> (&in)[PASS]) {
 #pragma unroll
     for (int e = 0; e < PASS; ++e) {
       const int i = row + ROWS * e + row0;
+      if (first + ROWS * e >= len) continue;
       if (i < 0 || i >= 16) continue;
       float x[8];
       in[e].values(x);
@@ -324,10 +346,10 @@ void step_kernel(DraftParams p) {
   take_slots(0, slots);
   take_drafts(0, drafts);
   if constexpr (NKT == 1) {
-    take_queries(n, queries);                          // (every token is in the one tile)
+    take_queries(0, n, queries);                          // (every token is in the one tile)
   } else {
     load_queries(-n, queries);
-    take_queries(0, queries);
+    take_queries(-n, 0, queries);
     for (int g = 1; 16 * g < n; ++g) {
       load_slots(g, slots);
       take_slots(g, slots);
@@ -357,18 +379,71 @@ void step_kernel(DraftParams p) {
   __syncthreads();
 
   auto operand = [&](const uint16_t* row) { return *(const v8bf*)(row + 8 * qq); };
-  // Projections of a tile's keys and queries on the wave's columns: [s] of strip s, tokens 4 qq + r.  Two strips and 32 keys
-  // at a time: all at once, the operands and sums are some 100 registers more.
+  // Projections of a tile's keys and queries on the wave's columns: [s] of strip s, tokens 4 qq + r.  What the operand's codes
+  // are too large by comes first: sums of the tokens' 32-key blocks (A) times offset and scale of the columns' blocks
+  // (B), one fp32 product a strip.  Then turns of 32 keys and two strips, a turn's sums scaled while the next one's products are
+  // formed; all at once, the operands and sums are some 100 registers more.
   auto project = [&](auto eight_bits, const uint16_t* rows, v4f (&xk)[SPW], v4f (&xq)[SPW]) {
     constexpr bool E8 = decltype(eight_bits)::value;
+    constexpr int PAIRS = SPW / 2;
     constexpr v4f none = {0.f, 0.f, 0.f, 0.f};
+    v8bf tk[2], tq[2][PIECES];                 // of 32 keys, the next ones ahead
+    auto fetch = [&](int kb) {
+      int own = l16;                           // (not earlier than its turn)
+      asm volatile("" : "+v"(own));
+      tk[kb & 1] = operand(rows + (size_t)own * SM::TS + 32 * kb);
 #pragma unroll
-    for (int s = 0; s < SPW; ++s) xk[s] = xq[s] = none;
+      for (int e = 0; e < PIECES; ++e) tq[kb & 1][e] = operand(&sm.q[16 * e + own][32 * kb]);
+    };
+    auto queries_times = [&](int kb, v8bf x, v4f acc) {
+#pragma unroll
+      for (int e = 0; e < PIECES; ++e) acc = mfma(tq[kb & 1][e], x, acc);
+      return acc;
+    };
+    if constexpr (BFS) {
+#pragma unroll
+      for (int s = 0; s < SPW; ++s) xk[s] = xq[s] = none;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        fetch(kb);
+#pragma unroll
+        for (int s = 0; s < SPW; ++s) {
+          const v8bf st = as_operand(raw[s][4 * kb], raw[s][4 * kb + 1], raw[s][4 * kb + 2], raw[s][4 * kb + 3]);
+          xk[s] = mfma(tk[kb & 1], st, xk[s]);
+          xq[s] = queries_times(kb, st, xq[s]);
+        }
+      }
+      return;
+    }
+    {
+      constexpr uint32_t one = 0x3F803F80u;
+      const v8bf ones = as_operand(one, one, one, one);
+      float sum_k = 0.f, sum_q = 0.f;          // of token l16's block qq
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        fetch(kb);
+        const float k = mfma(ones, tk[kb & 1], none)[0];
+        v4f acc = none;
+#pragma unroll
+        for (int e = 0; e < PIECES; ++e) acc = mfma(ones, tq[kb & 1][e], acc);
+        sum_k = qq == kb ? k : sum_k;
+        sum_q = qq == kb ? acc[0] : sum_q;
+      }
+      const int kb = KB == 4 ? qq : qq & 1;    // (two blocks: the sums of the others are zeros)
+#pragma unroll
+      for (int s = 0; s < SPW; s += 2) {
+        const uint32_t sc = *(const uint32_t*)&sm.m.s.s[kb][c0 + s], zp = *(const uint32_t*)&sm.m.s.z[kb][c0 + s];
+        const float f0 = bits_f32(sc << 16) * bits_f32(zp << 16), f1 = bits_f32(sc & 0xFFFF0000u) * bits_f32(zp & 0xFFFF0000u);
+        xk[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(sum_k, f0, none, 0, 0, 0);
+        xq[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(sum_q, f0, none, 0, 0, 0);
+        xk[s + 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(sum_k, f1, none, 0, 0, 0);
+        xq[s + 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(sum_q, f1, none, 0, 0, 0);
+      }
+    }
     v4f ak[2][2], aq[2][2];                    // [turn][strip of the pair]
     uint32_t sc[2];
-    // one turn's sums, scaled: while the next turn's products are formed
     auto add = [&](int turn) {
-      const int s0 = 2 * (turn / KB);
+      const int s0 = 2 * (turn % PAIRS);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const float scale = bits_f32(s ? sc[turn & 1] & 0xFFFF0000u : sc[turn & 1] << 16);
@@ -380,50 +455,19 @@ void step_kernel(DraftParams p) {
         asm volatile("" : "+v"(xk[s0 + s]), "+v"(xq[s0 + s]));
       }
     };
+    // (a mask in a vector register and a constant in a scalar one: one operation for both)
+    uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+    asm volatile("" : "+v"(mask), "+s"(sixteen));
+    fetch(0);
 #pragma unroll
-    for (int turn = 0; turn < SPW / 2 * KB; ++turn) {
-      const int s0 = 2 * (turn / KB), kb = turn % KB;
-      // (a turn's operands are not begun before it: they depend on these)
-      int own = l16;
-      asm volatile("" : "+v"(own));
-      if constexpr (!BFS)
+    for (int turn = 0; turn < PAIRS * KB; ++turn) {
+      const int kb = turn / PAIRS, s0 = 2 * (turn % PAIRS);
+      if (s0 == 0 && kb + 1 < KB) fetch(kb + 1);
 #pragma unroll
-        for (int s = s0; s < s0 + 2; ++s)
+      for (int s = s0; s < s0 + 2; ++s)
 #pragma unroll
-          for (int i = 0; i < (E8 ? 2 : 1); ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb + i : kb]));
-      const v8bf tk = operand(rows + (size_t)own * SM::TS + 32 * kb);
-      v8bf tq[PIECES];
-#pragma unroll
-      for (int e = 0; e < PIECES; ++e) tq[e] = operand(&sm.q[16 * e + own][32 * kb]);
-      auto queries_times = [&](v8bf x, v4f acc) {
-#pragma unroll
-        for (int e = 0; e < PIECES; ++e) acc = mfma(tq[e], x, acc);
-        return acc;
-      };
-      if constexpr (BFS) {
-#pragma unroll
-        for (int s = s0; s < s0 + 2; ++s) {
-          const v8bf st = as_operand(raw[s][4 * kb], raw[s][4 * kb + 1], raw[s][4 * kb + 2], raw[s][4 * kb + 3]);
-          xk[s] = mfma(tk, st, xk[s]);
-          xq[s] = queries_times(st, xq[s]);
-        }
-        continue;
-      }
-      v4f (&k)[2] = ak[turn & 1], (&q)[2] = aq[turn & 1];
+        for (int i = 0; i < (E8 ? 2 : 1); ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb + i : kb]));
       sc[turn & 1] = *(const uint32_t*)&sm.m.s.s[kb][c0 + s0];
-      if (asym) {
-        const uint32_t zp = *(const uint32_t*)&sm.m.s.z[kb][c0 + s0];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint32_t z = __builtin_amdgcn_perm(zp, zp, s ? 0x03020302u : 0x01000100u);
-          k[s] = mfma(tk, as_operand(z, z, z, z), none);
-          q[s] = queries_times(as_operand(z, z, z, z), none);
-        }
-      } else {                                 // symmetric: the same offset for every column, -24 or -128
-        const uint32_t z = E8 ? 0xC300C300u : 0xC1C0C1C0u;
-        k[0] = k[1] = mfma(tk, as_operand(z, z, z, z), none);
-        q[0] = q[1] = queries_times(as_operand(z, z, z, z), none);
-      }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         v8bf st;
@@ -438,15 +482,15 @@ void step_kernel(DraftParams p) {
           st = as_operand(w[0], w[1], w[2], w[3]);
         } else {
           const uint32_t y = raw[s0 + s][kb];
-          st = as_operand(((y << 3) & 0x00780078u) | 0x41804180u, ((y >> 5) & 0x00780078u) | 0x41804180u,
-                          ((y >> 1) & 0x00780078u) | 0x41804180u, ((y >> 9) & 0x00780078u) | 0x41804180u);
+          st = as_operand(((y << 3) & mask) | sixteen, ((y >> 5) & mask) | sixteen, ((y >> 1) & mask) | sixteen,
+                          ((y >> 9) & mask) | sixteen);
         }
-        k[s] = mfma(tk, st, k[s]);
-        q[s] = queries_times(st, q[s]);
+        ak[turn & 1][s] = mfma(tk[kb & 1], st, none);
+        aq[turn & 1][s] = queries_times(kb, st, none);
       }
       if (turn > 0) add(turn - 1);
     }
-    if constexpr (!BFS) add(SPW / 2 * KB - 1);
+    add(PAIRS * KB - 1);
   };
   // The decays and Gram products of a tile with the tokens before it, in the matrix unit's layout: token i = 16 t + l16 a lane,
   // tokens j 4 qq + r of 16 jt.  From the tile's own end back to the first token: D_ij is the product of the decays on i's path
@@ -509,12 +553,17 @@ void step_kernel(DraftParams p) {
   };
   // x += what the tokens below `end` add, four an instruction (fp32): weights at[j][l16], times sign
   auto add_tokens = [&](int end, const float (*at)[16], float sign, v4f (&x)[SPW]) {
-    for (int j = qq; j < end + qq; j += 4) {
-      const float w = sign * at[j][l16];
-      float u[SPW];
-      columns(sm.u[j], u);
+    for (int j0 = 0; j0 < end; j0 += 16) {     // (rows behind the last token are zeros)
+      float w[4], u[4][SPW];
 #pragma unroll
-      for (int s = 0; s < SPW; ++s) x[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, u[s], x[s], 0, 0, 0);
+      for (int f = 0; f < 4; ++f) {
+        w[f] = sign * at[j0 + 4 * f + qq][l16];
+        columns(sm.u[j0 + 4 * f + qq], u[f]);
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int s = 0; s < SPW; ++s) x[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[f], u[f][s], x[s], 0, 0, 0);
     }
   };
 
@@ -523,13 +572,13 @@ void step_kernel(DraftParams p) {
       if (t > 0) {
         __syncthreads();                       // the tile before is done with its queries and products
         load_queries(16 * t - n, queries);
-        take_queries(0, queries);
+        take_queries(16 * t - n, 0, queries);
         __syncthreads();
       }
     }
     v4f xk[SPW], xq[SPW];
-    if (is8) project(std::true_type{}, &sm.k[16 * t][0], xk, xq);
-    else project(std::false_type{}, &sm.k[16 * t][0], xk, xq);
+    if (!is8) project(std::false_type{}, &sm.k[16 * t][0], xk, xq);
+    else if constexpr (HB != 4) project(std::true_type{}, &sm.k[16 * t][0], xk, xq);
     if constexpr (NKT == 1) __syncthreads();   // the scales have been read: the Gram products take their place
     if (wave == 0) gram(std::false_type{}, t);
     else gram(std::true_type{}, t);
@@ -546,28 +595,36 @@ void step_kernel(DraftParams p) {
       for (int s = 0; s < SPW; ++s) xk[s][r] = be * v[s] - f * xk[s][r];
     }
     if (NKT > 1 && t > 0) add_tokens(16 * t, sm.m.g.a, -1.f, xk);
+    // four tokens at a time: they are in the lanes of one row, which solve their triangle; what they add to those behind them
+    // is one product a strip
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float* row = &sm.u[i0 + r][c0];
-      if constexpr (SPW == 4) *(float4*)row = make_float4(xk[0][r], xk[1][r], xk[2][r], xk[3][r]);
-      else *(float2*)row = make_float2(xk[0][r], xk[1][r]);
-    }
-    wave_sync();
-    if (lane < CW) {
-      const int c = wave * CW + lane;
-      float y[16];
+    for (int f = 0; f < 4; ++f) {
+      const float (*a)[16] = sm.m.g.a + 16 * t + 4 * f;
+      const float4 a0 = *(const float4*)&a[0][4 * f], a1 = *(const float4*)&a[1][4 * f];
+      const float a23 = a[2][4 * f + 3];
+      float y[4][SPW];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = sm.u[16 * t + i][c];
-#pragma unroll
-      for (int j = 0; j < 15; ++j) {
-        const float* a = sm.m.g.a[16 * t + j];
-#pragma unroll
-        for (int i = j + 1; i < 16; ++i) y[i] -= a[i] * y[j];
+      for (int s = 0; s < SPW; ++s) {
+        y[0][s] = xk[s][0];
+        y[1][s] = xk[s][1] - a0.y * y[0][s];
+        y[2][s] = xk[s][2] - a0.z * y[0][s] - a1.z * y[1][s];
+        y[3][s] = xk[s][3] - a0.w * y[0][s] - a1.w * y[1][s] - a23 * y[2][s];
       }
+      if (qq == f)
 #pragma unroll
-      for (int i = 1; i < 16; ++i) sm.u[16 * t + i][c] = y[i];
+        for (int r = 0; r < 4; ++r) {
+          float* row = &sm.u[i0 + r][c0];
+          if constexpr (SPW == 4) *(float4*)row = make_float4(y[r][0], y[r][1], y[r][2], y[r][3]);
+          else *(float2*)row = make_float2(y[r][0], y[r][1]);
+        }
+      wave_sync();
+      if (f == 3) break;
+      const float w = -a[qq][l16];
+      float u[SPW];
+      columns(sm.u[16 * t + 4 * f + qq], u);
+#pragma unroll
+      for (int s = 0; s < SPW; ++s) xk[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, u[s], xk[s], 0, 0, 0);
     }
-    wave_sync();
 
     // -------------------------------------------------------------- outputs
     if (16 * t + 16 <= n) continue;            // buffered tokens only
@@ -591,12 +648,18 @@ void step_kernel(DraftParams p) {
 template <int D, int NKT, bool BF16>
 hipError_t launch(const DraftParams& p, int buf_kind, hipStream_t s) {
   const dim3 grid((unsigned)p.l.Hv, (unsigned)p.l.B);
+  // (all heads in 4 bits, bf16: 16 registers fewer, and no second way through the projections)
+  constexpr int H4 = BF16 ? 4 : 0;
   if (p.l.bf16_state)                          // (int8 buffer only: checked by the caller)
-    step_kernel<D, NKT, BF16, false, true><<<grid, kThreads, 0, s>>>(p);
+    step_kernel<D, NKT, BF16, false, 4, true><<<grid, kThreads, 0, s>>>(p);
+  else if (buf_kind == PACE_BUF_INT8 && p.l.mask8 == 0)
+    step_kernel<D, NKT, BF16, false, H4, false><<<grid, kThreads, 0, s>>>(p);
   else if (buf_kind == PACE_BUF_INT8)
-    step_kernel<D, NKT, BF16, false, false><<<grid, kThreads, 0, s>>>(p);
+    step_kernel<D, NKT, BF16, false, 0, false><<<grid, kThreads, 0, s>>>(p);
+  else if (p.l.mask8 == 0)
+    step_kernel<D, NKT, BF16, true, H4, false><<<grid, kThreads, 0, s>>>(p);
   else
-    step_kernel<D, NKT, BF16, true, false><<<grid, kThreads, 0, s>>>(p);
+    step_kernel<D, NKT, BF16, true, 0, false><<<grid, kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

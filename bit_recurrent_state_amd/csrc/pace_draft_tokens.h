@@ -29,8 +29,8 @@ __device__ inline float token_max(float x) {
 template <bool BF16>
 struct Raw8 {
   uint32_t w[BF16 ? 4 : 8];
-  __device__ void load(const void* p, int64_t at) {
-    const uint4* from = (const uint4*)((const uint8_t*)p + at * (BF16 ? 2 : 4));
+  __device__ void load(const void* p) {
+    const uint4* from = (const uint4*)p;
 #pragma unroll
     for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
       const uint4 v = from[i];
@@ -48,7 +48,7 @@ struct Raw8 {
 template <bool BF16>
 __device__ inline void load8(const void* p, int64_t at, float (&x)[8]) {
   Raw8<BF16> r;
-  r.load(p, at);
+  r.load((const uint8_t*)p + at * (BF16 ? 2 : 4));
   r.values(x);
 }
 
