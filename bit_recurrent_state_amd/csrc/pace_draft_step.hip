@@ -178,16 +178,14 @@ void step_kernel(DraftParams p) {
   };
   Slots slots;
   load_slots(0, slots);
-  Drafts drafts;
+  Drafts drafts, more;
   load_drafts(0, drafts);
+  if constexpr (NKT > 1) load_drafts(1, more);
   Raw8<BF16> queries[PASS];
   if constexpr (NKT == 1) load_queries(0, queries);
-  uint64_t bitsrow = ~0ull;
-  if (p.tree) {
-    const int words = (T + 31) / 32;
-    const uint32_t* t = p.tree + b * p.tree_stride + (int64_t)min(tid, T - 1) * words;
-    bitsrow = t[0] | (words > 1 ? (uint64_t)t[words - 1] << 32 : 0ull);
-  }
+  const int words = (T + 31) / 32;
+  const uint32_t* const bits_at = p.tree ? p.tree + b * p.tree_stride + min(tid, T - 1) * words : (const uint32_t*)l.buffer;
+  const uint32_t bits_lo = bits_at[0], bits_hi = bits_at[words - 1];   // (a chain: whatever the buffer begins with, not used)
 
   // ------------------------------------------------------------------ state
   const bool is8 = HB != 4 && !BFS && ((l.mask8 >> h) & 1ull) != 0, asym = l.asym != 0;
@@ -235,7 +233,7 @@ void step_kernel(DraftParams p) {
     for (int kb = 0; kb < KB; ++kb) {
       const int i = column * NG + kb / kpg;
       column_s[kb] = scales[i];
-      if (asym) column_z[kb] = is8 ? zeros[i] : (uint8_t)((zeros[i >> 1] >> (4 * (i & 1))) & 15);
+      if (asym) column_z[kb] = zeros[is8 ? i : i >> 1];
     }
   }
 
@@ -349,12 +347,14 @@ void step_kernel(DraftParams p) {
     take_queries(0, n, queries);                          // (every token is in the one tile)
   } else {
     load_queries(-n, queries);
+    take_drafts(1, more);
     take_queries(-n, 0, queries);
+    load_queries(16 - n, queries);                     // (the next tile's)
     for (int g = 1; 16 * g < n; ++g) {
       load_slots(g, slots);
       take_slots(g, slots);
     }
-    for (int g = 1; 16 * g < len; ++g) {
+    for (int g = 2; 16 * g < len; ++g) {
       load_drafts(g, drafts);
       take_drafts(g, drafts);
     }
@@ -365,13 +365,15 @@ void step_kernel(DraftParams p) {
     *(float4*)&sm.u[i][e0 + 4] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (e0 == 0) sm.ks[i] = sm.decay[i] = sm.beta[i] = 0.f;
   }
-  if (tid < len) sm.row[tid] = bitsrow;
+  if (tid < len) sm.row[tid] = p.tree ? bits_lo | (words > 1 ? (uint64_t)bits_hi << 32 : 0ull) : ~0ull;
   if constexpr (!BFS) {
     if (tid < D) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         sm.m.s.s[kb][tid] = column_s[kb];
-        const float z = asym ? (float)column_z[kb] : (float)(1 << (bits - 1));
+        const int odd = (tid * (KB * 32 / l.group) + kb * 32 / l.group) & 1;   // (4 bits: two zero points a byte)
+        const int zp = is8 ? column_z[kb] : (column_z[kb] >> (4 * odd)) & 15;
+        const float z = asym ? (float)zp : (float)(1 << (bits - 1));
         sm.m.s.z[kb][tid] = (uint16_t)two_bf16(-((is8 ? 0.f : 16.f) + z), 0.f);
       }
     }
@@ -571,8 +573,8 @@ void step_kernel(DraftParams p) {
     if constexpr (NKT > 1) {
       if (t > 0) {
         __syncthreads();                       // the tile before is done with its queries and products
-        load_queries(16 * t - n, queries);
         take_queries(16 * t - n, 0, queries);
+        load_queries(16 * (t + 1) - n, queries);
         __syncthreads();
       }
     }
