@@ -39,19 +39,48 @@ def _declare():
 _declare()
 
 
+def _at(t, name, dtype, numel):
+    """_ptr of a required tensor, with one test where nothing is wrong."""
+    try:
+        if t.dtype is dtype and t.numel() == numel and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, name, dtype, numel)
+
+
 # ------------------------------------------------------------------ gated-delta layers
+
+_layers = {}
+
+
+def _layer(cfg: LayerConfig):
+    """(C configuration, state bytes, buffer bytes) of what a layer's configuration says now: worked out once for every
+    set of values, as it takes longer than the rest of a call's host side."""
+    bits = cfg.head_bits
+    key = (cfg.B, cfg.Hv, cfg.Hk, cfg.dk, cfg.dv, cfg.group, cfg.asym, cfg.buf, cfg.bf16_io, cfg.dP, cfg.chunk,
+           cfg.bf16_state, None if bits is None else tuple(bits))
+    known = _layers.get(key)
+    if known is None:
+        sizes = layout(cfg)
+        if len(_layers) >= 256:
+            _layers.clear()
+        known = _layers[key] = (cfg._c(), sizes["state_bytes"], sizes["buffer_bytes"])
+    return known
+
 
 def _layer_args(cfg: LayerConfig, state, buffer, k, v, a, beta):
     """(config, state, buffer), (k, v, a, beta), T of a call on drafts [B, T, ..]."""
-    if a.dim() != 3 or a.shape[0] != cfg.B or a.shape[2] != cfg.Hv:
-        raise ValueError(f"a has shape {tuple(a.shape)}, expected ({cfg.B}, T, {cfg.Hv})")
-    T, sizes, c = a.shape[1], layout(cfg), cfg._c()
-    io = torch.bfloat16 if cfg.bf16_io else torch.float32
-    n = cfg.B * T
-    return (c, (ctypes.byref(c), _ptr(state, "state", torch.uint8, sizes["state_bytes"]),
-                _ptr(buffer, "buffer", torch.uint8, sizes["buffer_bytes"])),
-            (_ptr(k, "k", io, n * cfg.Hk * cfg.dk), _ptr(v, "v", io, n * cfg.Hv * cfg.dv),
-             _ptr(a, "a", torch.float32, n * cfg.Hv), _ptr(beta, "beta", torch.float32, n * cfg.Hv)), T, io)
+    c, state_bytes, buffer_bytes = _layer(cfg)
+    B, Hv, d, f32 = cfg.B, cfg.Hv, cfg.dk, torch.float32
+    if a.dim() != 3 or a.shape[0] != B or a.shape[2] != Hv:
+        raise ValueError(f"a has shape {tuple(a.shape)}, expected ({B}, T, {Hv})")
+    T = a.shape[1]
+    io = torch.bfloat16 if cfg.bf16_io else f32
+    n = B * T
+    return (c, (ctypes.byref(c), _at(state, "state", torch.uint8, state_bytes), _at(buffer, "buffer", torch.uint8, buffer_bytes)),
+            (_at(k, "k", io, n * cfg.Hk * d), _at(v, "v", io, n * Hv * d), _at(a, "a", f32, n * Hv),
+             _at(beta, "beta", f32, n * Hv)), T, io)
 
 
 def _step_args(cfg, state, buffer, q, k, v, a, beta, o, tree, draft_lens, stream):
@@ -62,9 +91,9 @@ def _step_args(cfg, state, buffer, q, k, v, a, beta, o, tree, draft_lens, stream
             raise ValueError(f"tree has shape {tuple(tree.shape)}, expected ({cfg.B} or 1, {T}, {words})")
         step = T * words if tree.shape[0] == cfg.B else 0
     n = cfg.B * T
-    return (c, (*head, _ptr(q, "q", io, n * cfg.Hk * cfg.dk), *tokens, T,
+    return (c, (*head, _at(q, "q", io, n * cfg.Hk * cfg.dk), *tokens, T,
                 _ptr(draft_lens, "draft_lens", torch.int32, cfg.B, optional=True),
-                _ptr(tree, "tree", torch.int32, optional=True), step, _ptr(o, "o", io, n * cfg.Hv * cfg.dv), _stream(stream)))
+                _ptr(tree, "tree", torch.int32, optional=True), step, _at(o, "o", io, n * cfg.Hv * cfg.dv), _stream(stream)))
 
 
 def draft_step(cfg: LayerConfig, state, buffer, q, k, v, a, beta, o, tree=None, draft_lens=None, stream=None):
@@ -92,7 +121,7 @@ def _commit_args(cfg, state, buffer, k, v, a, beta, nodes, counts, workspace, mo
     c, head, tokens, T, _ = _layer_args(cfg, state, buffer, k, v, a, beta)
     if tuple(nodes.shape) != (cfg.B, T):
         raise ValueError(f"nodes has shape {tuple(nodes.shape)}, expected ({cfg.B}, {T})")
-    return (c, (*head, *tokens, T, _ptr(nodes, "nodes", torch.int32), _ptr(counts, "counts", torch.int32, cfg.B),
+    return (c, (*head, *tokens, T, _at(nodes, "nodes", torch.int32, cfg.B * T), _at(counts, "counts", torch.int32, cfg.B),
                 T if most is None else most, _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)))
 
 
@@ -165,10 +194,10 @@ def _verify_args(cfg, target, tokens, parents, uniforms, nodes, counts, next_tok
             raise ValueError(f"parents has shape {tuple(parents.shape)}, expected ({cfg.B} or 1, {cfg.T})")
         step = cfg.T if parents.shape[0] == cfg.B else 0
     i32 = torch.int32
-    return (ctypes.byref(cfg._c), tp, ts, dp, ds, _ptr(tokens, "tokens", i32, n),
-            _ptr(parents, "parents", i32, optional=True), step, _ptr(uniforms, "uniforms", torch.float32, n),
-            _ptr(draft_lens, "draft_lens", i32, cfg.B, optional=True), _ptr(nodes, "nodes", i32, n),
-            _ptr(counts, "counts", i32, cfg.B), _ptr(next_tokens, "next_tokens", i32, cfg.B),
+    return (ctypes.byref(cfg._c), tp, ts, dp, ds, _at(tokens, "tokens", i32, n),
+            _ptr(parents, "parents", i32, optional=True), step, _at(uniforms, "uniforms", torch.float32, n),
+            _ptr(draft_lens, "draft_lens", i32, cfg.B, optional=True), _at(nodes, "nodes", i32, n),
+            _at(counts, "counts", i32, cfg.B), _at(next_tokens, "next_tokens", i32, cfg.B),
             _ptr(workspace, "workspace", torch.uint8, optional=True),
             workspace.numel() if workspace is not None else 0, _stream(stream))
 
@@ -202,10 +231,10 @@ def _move_args(cfg, cache, src_table, dst_table, start, counts, nodes, most, str
     elif most is None:
         raise ValueError("most is required without nodes")
     pages = cfg.B * cfg.max_pages
-    return (ctypes.byref(cfg._c), _ptr(cache, "cache", torch.uint8, cfg._bytes),
-            _ptr(src_table, "src_table", torch.int32, pages), _ptr(dst_table, "dst_table", torch.int32, pages),
-            _ptr(start, "start", torch.int32, cfg.B), _ptr(nodes, "nodes", torch.int32, optional=True),
-            nodes.shape[1] if nodes is not None else 0, _ptr(counts, "counts", torch.int32, cfg.B), most, _stream(stream))
+    return (ctypes.byref(cfg._c), _at(cache, "cache", torch.uint8, cfg._bytes),
+            _at(src_table, "src_table", torch.int32, pages), _at(dst_table, "dst_table", torch.int32, pages),
+            _at(start, "start", torch.int32, cfg.B), _ptr(nodes, "nodes", torch.int32, optional=True),
+            nodes.shape[1] if nodes is not None else 0, _at(counts, "counts", torch.int32, cfg.B), most, _stream(stream))
 
 
 def cache_move(cfg: CacheConfig, cache, src_table, dst_table, start, counts, nodes=None, most=None, stream=None):

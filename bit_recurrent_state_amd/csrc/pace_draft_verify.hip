@@ -42,15 +42,26 @@ __device__ inline double lane_double(double x, int lane) {
   return bits_f64((uint64_t)hi << 32 | lo);
 }
 
-// Inclusive sums over the lanes of a wave.
-__device__ inline double wave_scan(double x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+// Sums over the lanes of a wave, by lane moves on the vector unit: rows of 16 first (shifts by 1, 2, 4, 8), then the sums of
+// the rows before them.
+template <int CTRL, int ROWS>
+__device__ inline double moved(double x) {   // 0 where nothing is moved to
+  const uint64_t u = f64_bits(x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+  return bits_f64((uint64_t)hi << 32 | lo);
+}
+// (lane l: of lanes 0 .. l)
+__device__ inline double wave_scan(double x) {
+  x += moved<0x111, 0xF>(x);
+  x += moved<0x112, 0xF>(x);
+  x += moved<0x114, 0xF>(x);
+  x += moved<0x118, 0xF>(x);
+  x += moved<0x142, 0xA>(x);                  // lane 15 of a row to the next one's lanes: rows 1 and 3
+  x += moved<0x143, 0xC>(x);                  // lane 31 to rows 2 and 3
   return x;
 }
+__device__ inline double wave_sum(double x) { return lane_double(wave_scan(x), 63); }
 
 // The walk's state, and what of it a second kernel needs.
 struct Walk {
@@ -204,18 +215,14 @@ __device__ inline double chunk_sum(const Row<E>& r, int chunk, int lane) {
     weights(r, chunk * kVerifyChunk + j * 512 + lane * 8, w);
     sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  return sum;
+  return wave_sum(sum);
 }
 
 // Sum of n values, the same in every lane.
 __device__ inline double total_of(const double* sums, int n, int lane) {
   double t = 0.0;
   for (int i = lane; i < n; i += 64) t += sums[i];
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) t += __shfl_xor(t, d);
-  return t;
+  return wave_sum(t);
 }
 
 // The sums of a row's chunks by the waves of a workgroup, and their total.
@@ -230,14 +237,24 @@ __device__ inline double row_sums(const VerifyParams& p, const Row<E>& r, double
   return total_of(sums, p.chunks, lane);
 }
 
-// The first token whose sum from the row's start passes u total, or the last of any weight.  One wave; total > 0.
+// The first token whose sum from the row's start passes u total, or the last of any weight; total > 0.  All waves find the
+// chunk; four of them look at a quarter of it each.  Written to *next by one thread.
 template <typename E>
-__device__ inline int token_at(const VerifyParams& p, const Row<E>& row, const double* sums, double u, double total, int lane) {
+__device__ inline void token_at(const VerifyParams& p, const Row<E>& row, const double* sums, double u, double total, int32_t* next) {
+  constexpr int PARTS = kPer / 8;
+  __shared__ double part_sum[PARTS];
+  __shared__ int32_t part_last[PARTS], hit[PARTS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (wave >= PARTS && blockDim.x > 64 * PARTS) {
+    __syncthreads();
+    __syncthreads();
+    return;
+  }
   double r = u * total, before = 0.0, found = 0.0;
   int chunk = -1, last = 0;
   for (int i = 0; i < p.chunks && chunk < 0; i += 64) {
     const double t = i + lane < p.chunks ? sums[i + lane] : 0.0;
-    const double upto = before + wave_scan(t, lane);
+    const double upto = before + wave_scan(t);
     const uint64_t over = __ballot(upto > r), any = __ballot(t > 0.0);
     if (over) {
       const int l = __builtin_ctzll(over);
@@ -252,40 +269,49 @@ __device__ inline int token_at(const VerifyParams& p, const Row<E>& row, const d
     chunk = last;
     r = HUGE_VAL;
   }
-  int tail = 0;
-  before = found;
-  for (int j = 0; j < kPer / 8; ++j) {
-    const int v0 = chunk * kVerifyChunk + j * 512 + lane * 8;
-    double w[8];
-    weights(row, v0, w);
-    double t = 0.0;
-    int high = -1;
+  const int v0 = chunk * kVerifyChunk + wave * 512 + lane * 8;
+  double w[8];
+  weights(row, v0, w);
+  double t = 0.0;
+  int high = -1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      t += w[i];
-      if (w[i] > 0.0) high = i;
-    }
-    const double upto = before + wave_scan(t, lane);
-    double e = __shfl_up(upto, 1);
-    if (lane == 0) e = before;
-    int mine = -1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      e += w[i];
-      if (mine < 0 && e > r && w[i] > 0.0) mine = i;
-    }
-    const uint64_t over = __ballot(mine >= 0), any = __ballot(high >= 0);
-    if (over) {
-      const int l = __builtin_ctzll(over);
-      return chunk * kVerifyChunk + j * 512 + l * 8 + __builtin_amdgcn_readlane(mine, l);
-    }
-    if (any) {
-      const int l = 63 - __builtin_clzll(any);
-      tail = chunk * kVerifyChunk + j * 512 + l * 8 + __builtin_amdgcn_readlane(high, l);
-    }
-    before = lane_double(upto, 63);
+  for (int i = 0; i < 8; ++i) {
+    t += w[i];
+    if (w[i] > 0.0) high = i;
   }
-  return tail;
+  const double upto = wave_scan(t);
+  if (lane == 63) part_sum[wave] = upto;
+  __syncthreads();
+  double e = found;                      // the sums from the left: of the parts before, of the lanes before, of the tokens
+#pragma unroll
+  for (int j = 0; j < PARTS; ++j)
+    if (j < wave) e += part_sum[j];
+  const double left = moved<0x138, 0xF>(upto);   // lane l - 1's
+  e += lane ? left : 0.0;
+  int mine = -1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    e += w[i];
+    if (mine < 0 && e > r && w[i] > 0.0) mine = i;
+  }
+  const uint64_t over = __ballot(mine >= 0), any = __ballot(high >= 0);
+  const int lo = over ? __builtin_ctzll(over) : 0, la = any ? 63 - __builtin_clzll(any) : 0;
+  const int base = chunk * kVerifyChunk + wave * 512;
+  const int hit_at = __builtin_amdgcn_readlane(mine, lo), last_at = __builtin_amdgcn_readlane(high, la);
+  if (lane == 0) {
+    hit[wave] = over ? base + lo * 8 + hit_at : -1;
+    part_last[wave] = any ? base + la * 8 + last_at : -1;
+  }
+  __syncthreads();
+  if (threadIdx.x > 0) return;
+  int token = -1;
+#pragma unroll
+  for (int j = PARTS - 1; j >= 0; --j)
+    if (hit[j] >= 0) token = hit[j];
+#pragma unroll
+  for (int j = PARTS - 1; j >= 0; --j)
+    if (token < 0) token = part_last[j];
+  *next = token;
 }
 
 template <typename E>
@@ -312,9 +338,10 @@ __device__ inline void finish(const VerifyParams& p, int b, const Walk& w, const
     __syncthreads();
     total = row_sums(p, row, sums);
   }
-  if (tid >= 64) return;
-  const int token = total > 0.0 ? token_at(p, row, sums, uniform(p.uniforms[(int64_t)b * p.T]), total, tid) : -1;
-  if (tid == 0) p.next[b] = token;
+  if (total > 0.0)
+    token_at(p, row, sums, uniform(p.uniforms[(int64_t)b * p.T]), total, p.next + b);
+  else if (tid == 0)
+    p.next[b] = -1;
 }
 
 // The walk from where it stands to its end, and the results.  One workgroup.  total: of the row that the walk waits for.
@@ -337,22 +364,21 @@ __device__ inline void go_on(const VerifyParams& p, Shared<NODES>& s, int b, int
   finish(p, b, s.w, s.path, row_of<E>(p, b, s.w, s.gone), sums, total);
 }
 
-__device__ inline bool nothing_to_do(const VerifyParams& p, int b) {
-  if (!p.draft_lens || p.draft_lens[b] > 0) return false;
+// A sequence without drafts.
+__device__ inline void nothing(const VerifyParams& p, int b) {
   for (int i = threadIdx.x; i < p.T; i += blockDim.x) p.nodes[(int64_t)b * p.T + i] = -1;
   if (threadIdx.x == 0) {
     p.counts[b] = 0;
     p.next[b] = -1;
   }
-  return true;
 }
 
 template <typename E, int NODES>
 __global__ __launch_bounds__(kThreads) void verify_kernel(VerifyParams p) {
   __shared__ Shared<NODES> s;
   const int b = blockIdx.x;
-  if (nothing_to_do(p, b)) return;
   const int len = begin(p, s, b, target_of<E>(p, b), draft_of<E>(p, b));
+  if (len == 0) return nothing(p, b);
   go_on<E>(p, s, b, len, p.chunks <= kLdsChunks ? s.sums : scratch_of(p, b).sums, 0.0);
 }
 
@@ -363,8 +389,8 @@ template <typename E, int NODES>
 __global__ __launch_bounds__(kSumThreads) void sums_kernel(VerifyParams p) {
   __shared__ Shared<NODES> s;
   const int b = blockIdx.y, tid = threadIdx.x;
-  if (p.draft_lens && p.draft_lens[b] <= 0) return;
   const int len = begin(p, s, b, target_of<E>(p, b), draft_of<E>(p, b));
+  if (len == 0) return;
   if (tid < 64) walk(s, len, p.draft != nullptr, tid);
   __syncthreads();
   const Scratch to = scratch_of(p, b);
@@ -385,9 +411,9 @@ template <typename E, int NODES>
 __global__ __launch_bounds__(kThreads) void finish_kernel(VerifyParams p) {
   __shared__ Shared<NODES> s;
   const int b = blockIdx.x, tid = threadIdx.x;
-  if (nothing_to_do(p, b)) return;
   const Scratch from = scratch_of(p, b);
-  const Walk w = *from.w;
+  const Walk w = *from.w;                // (of a sequence without drafts: whatever lay there, not used)
+  if (p.draft_lens && p.draft_lens[b] <= 0) return nothing(p, b);
   const double total = total_of(from.sums, p.chunks, tid & 63);
   if (!w.more) {
     finish(p, b, w, from.path, row_of<E>(p, b, w, from.gone), from.sums, total);
