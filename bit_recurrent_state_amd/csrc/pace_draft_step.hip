@@ -83,9 +83,9 @@ __device__ inline uint4 in_order(const float (&x)[8]) {
   return make_uint4(two_bf16(x[0], x[2]), two_bf16(x[1], x[3]), two_bf16(x[4], x[6]), two_bf16(x[5], x[7]));
 }
 
-// HB: 4 = every head 4-bit, 0 = by the head map.
-template <int D, int NKT, bool BF16, bool MIXED, int HB, bool BFS>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS ? (HB == 4 && NKT == 1 ? 4 : 3) : 1)))
+// HB: 4 = every head 4-bit, 0 = by the head map.  KPS: 32-key blocks that are sure to share a scale (group / 32, or 1).
+template <int D, int NKT, bool BF16, bool MIXED, int HB, int KPS, bool BFS>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS ? (NKT == 1 ? 4 : 3) : 1)))
 void step_kernel(DraftParams p) {
   constexpr int PIECES = BF16 ? 1 : 3;
   using SM = Smem<D, NKT, PIECES>;
@@ -221,17 +221,18 @@ void step_kernel(DraftParams p) {
       raw[s][0] = v.x; raw[s][1] = v.y;
     }
   }
-  // a thread's column of scales and zero points
+  // a thread's column of scales and zero points (groups of 32 keys, or 64)
+  const int wide = l.group == 64;
   uint16_t column_s[KB];
   uint8_t column_z[KB];
   const int column = min(tid, D - 1);
   if constexpr (!BFS) {
-    const int kpg = l.group / 32, NG = KB / kpg;
+    const int NG = KB >> wide;
     const uint16_t* scales = (const uint16_t*)(rec + (is8 ? l.scales_off8 : l.scales_off4));
     const uint8_t* zeros = rec + (is8 ? l.zeros_off8 : l.zeros_off4);
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      const int i = column * NG + kb / kpg;
+      const int i = column * NG + (kb >> wide);
       column_s[kb] = scales[i];
       if (asym) column_z[kb] = zeros[is8 ? i : i >> 1];
     }
@@ -325,6 +326,18 @@ void step_kernel(DraftParams p) {
       const int i = row + ROWS * e + row0;
       if (first + ROWS * e >= len) continue;
       if (i < 0 || i >= 16) continue;
+      if constexpr (BF16) {                    // (exact as they are)
+        const uint32_t* const w = in[e].w;
+        uint4 y = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (!BFS) {
+          y.x = __builtin_amdgcn_perm(w[1], w[0], 0x05040100u);
+          y.y = __builtin_amdgcn_perm(w[1], w[0], 0x07060302u);
+          y.z = __builtin_amdgcn_perm(w[3], w[2], 0x05040100u);
+          y.w = __builtin_amdgcn_perm(w[3], w[2], 0x07060302u);
+        }
+        *(uint4*)&sm.q[i][e0] = y;
+        continue;
+      }
       float x[8];
       in[e].values(x);
 #pragma unroll
@@ -371,7 +384,7 @@ void step_kernel(DraftParams p) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         sm.m.s.s[kb][tid] = column_s[kb];
-        const int odd = (tid * (KB * 32 / l.group) + kb * 32 / l.group) & 1;   // (4 bits: two zero points a byte)
+        const int odd = (tid * (KB >> wide) + (kb >> wide)) & 1;   // (4 bits: two zero points a byte)
         const int zp = is8 ? column_z[kb] : (column_z[kb] >> (4 * odd)) & 15;
         const float z = asym ? (float)zp : (float)(1 << (bits - 1));
         sm.m.s.z[kb][tid] = (uint16_t)two_bf16(-((is8 ? 0.f : 16.f) + z), 0.f);
@@ -460,39 +473,49 @@ void step_kernel(DraftParams p) {
     // (a mask in a vector register and a constant in a scalar one: one operation for both)
     uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
     asm volatile("" : "+v"(mask), "+s"(sixteen));
-    fetch(0);
+    constexpr int TURNS = PAIRS * KB / KPS;
+    if constexpr (KPS == 1) fetch(0);
 #pragma unroll
-    for (int turn = 0; turn < PAIRS * KB; ++turn) {
-      const int kb = turn / PAIRS, s0 = 2 * (turn % PAIRS);
-      if (s0 == 0 && kb + 1 < KB) fetch(kb + 1);
+    for (int turn = 0; turn < TURNS; ++turn) {
+      const int kb0 = turn / PAIRS * KPS, s0 = 2 * (turn % PAIRS);
+      if (s0 == 0) {
+        if constexpr (KPS == 1) {
+          if (kb0 + 1 < KB) fetch(kb0 + 1);
+        } else {
+          fetch(kb0);
+          fetch(kb0 + 1);
+        }
+      }
 #pragma unroll
       for (int s = s0; s < s0 + 2; ++s)
 #pragma unroll
-        for (int i = 0; i < (E8 ? 2 : 1); ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb + i : kb]));
-      sc[turn & 1] = *(const uint32_t*)&sm.m.s.s[kb][c0 + s0];
+        for (int i = 0; i < (E8 ? 2 : 1) * KPS; ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb0 + i : kb0 + i]));
+      sc[turn & 1] = *(const uint32_t*)&sm.m.s.s[kb0][c0 + s0];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        v8bf st;
-        if constexpr (E8) {
-          uint32_t w[4];
+      for (int kb = kb0; kb < kb0 + KPS; ++kb)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t y = raw[s0 + s][2 * kb + e];
-            w[2 * e] = two_bf16((float)(y & 255u), (float)((y >> 16) & 255u));
-            w[2 * e + 1] = two_bf16((float)((y >> 8) & 255u), (float)(y >> 24));
+        for (int s = 0; s < 2; ++s) {
+          v8bf st;
+          if constexpr (E8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t y = raw[s0 + s][2 * kb + e];
+              w[2 * e] = two_bf16((float)(y & 255u), (float)((y >> 16) & 255u));
+              w[2 * e + 1] = two_bf16((float)((y >> 8) & 255u), (float)(y >> 24));
+            }
+            st = as_operand(w[0], w[1], w[2], w[3]);
+          } else {
+            const uint32_t y = raw[s0 + s][kb];
+            st = as_operand(((y << 3) & mask) | sixteen, ((y >> 5) & mask) | sixteen, ((y >> 1) & mask) | sixteen,
+                            ((y >> 9) & mask) | sixteen);
           }
-          st = as_operand(w[0], w[1], w[2], w[3]);
-        } else {
-          const uint32_t y = raw[s0 + s][kb];
-          st = as_operand(((y << 3) & mask) | sixteen, ((y >> 5) & mask) | sixteen, ((y >> 1) & mask) | sixteen,
-                          ((y >> 9) & mask) | sixteen);
+          ak[turn & 1][s] = mfma(tk[kb & 1], st, kb > kb0 ? ak[turn & 1][s] : none);
+          aq[turn & 1][s] = queries_times(kb, st, kb > kb0 ? aq[turn & 1][s] : none);
         }
-        ak[turn & 1][s] = mfma(tk[kb & 1], st, none);
-        aq[turn & 1][s] = queries_times(kb, st, none);
-      }
       if (turn > 0) add(turn - 1);
     }
-    add(PAIRS * KB - 1);
+    add(TURNS - 1);
   };
   // The decays and Gram products of a tile with the tokens before it, in the matrix unit's layout: token i = 16 t + l16 a lane,
   // tokens j 4 qq + r of 16 jt.  From the tile's own end back to the first token: D_ij is the product of the decays on i's path
@@ -569,7 +592,7 @@ void step_kernel(DraftParams p) {
     }
   };
 
-  for (int t = 0; t < NT; ++t) {
+  for (int t = 0; t < (NKT == 1 ? 1 : NT); ++t) {
     if constexpr (NKT > 1) {
       if (t > 0) {
         __syncthreads();                       // the tile before is done with its queries and products
@@ -650,18 +673,18 @@ void step_kernel(DraftParams p) {
 template <int D, int NKT, bool BF16>
 hipError_t launch(const DraftParams& p, int buf_kind, hipStream_t s) {
   const dim3 grid((unsigned)p.l.Hv, (unsigned)p.l.B);
-  // (all heads in 4 bits, bf16: 16 registers fewer, and no second way through the projections)
-  constexpr int H4 = BF16 ? 4 : 0;
-  if (p.l.bf16_state)                          // (int8 buffer only: checked by the caller)
-    step_kernel<D, NKT, BF16, false, 4, true><<<grid, kThreads, 0, s>>>(p);
-  else if (buf_kind == PACE_BUF_INT8 && p.l.mask8 == 0)
-    step_kernel<D, NKT, BF16, false, H4, false><<<grid, kThreads, 0, s>>>(p);
-  else if (buf_kind == PACE_BUF_INT8)
-    step_kernel<D, NKT, BF16, false, 0, false><<<grid, kThreads, 0, s>>>(p);
-  else if (p.l.mask8 == 0)
-    step_kernel<D, NKT, BF16, true, H4, false><<<grid, kThreads, 0, s>>>(p);
-  else
-    step_kernel<D, NKT, BF16, true, 0, false><<<grid, kThreads, 0, s>>>(p);
+  const bool mixed = buf_kind == PACE_BUF_K4_VBF16;
+  if (p.l.bf16_state) {                        // (int8 buffer only: checked by the caller)
+    step_kernel<D, NKT, BF16, false, 4, 1, true><<<grid, kThreads, 0, s>>>(p);
+  } else if (BF16 && p.l.mask8 == 0 && !mixed && p.l.group == 64) {
+    // All heads in 4 bits, the symmetric layout's groups: 16 registers fewer, no second way through the projections, half
+    // as many scalings.  64 x 8 drafts: 15.5 us, by the general kernel 16.1; one sequence's five: 6.4 and 6.8.
+    if constexpr (BF16) step_kernel<D, NKT, true, false, 4, 2, false><<<grid, kThreads, 0, s>>>(p);
+  } else if (mixed) {
+    step_kernel<D, NKT, BF16, true, 0, 1, false><<<grid, kThreads, 0, s>>>(p);
+  } else {
+    step_kernel<D, NKT, BF16, false, 0, 1, false><<<grid, kThreads, 0, s>>>(p);
+  }
   return hipGetLastError();
 }
 
