@@ -1,6 +1,6 @@
 // Gated-delta outputs of drafted tokens (include/pace_draft.h: pace_draft_step) -- gfx950, wave64.
 //
-// One workgroup of two waves per (sequence, value head) tile; nothing is written but o.  With S_0 the dequantised state and
+// One workgroup of two or four waves per (sequence, value head) tile; nothing is written but o.  With S_0 the dequantised state and
 // tokens 0 .. N-1 the n buffered ones and then the drafts, D_ij the product of the decays behind token j up to i along
 // the path of i, and Gamma_i the product of all of them (from S_0 on),
 //     u_i = beta_i (v_i - Gamma_i S_0^T k_i - sum_{j before i} D_ij (k_j . k_i) u_j)
@@ -26,7 +26,12 @@
 namespace pace {
 namespace {
 
-constexpr int kWaves = 2, kThreads = 64 * kWaves;
+// Waves of a workgroup: two where one tile holds all tokens (eight such workgroups a compute unit), four beyond it
+// (LDS leaves four, or fewer).
+template <int D, int NKT>
+constexpr int waves_of() {
+  return NKT == 1 || D == 64 ? 2 : 4;
+}
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -85,8 +90,9 @@ __device__ inline uint4 in_order(const float (&x)[8]) {
 
 // HB: 4 = every head 4-bit, 0 = by the head map.  KPS: 32-key blocks that are sure to share a scale (group / 32, or 1).
 template <int D, int NKT, bool BF16, bool MIXED, int HB, int KPS, bool BFS>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS ? (NKT == 1 ? 4 : 3) : 1)))
+__global__ __launch_bounds__((64 * waves_of<D, NKT>())) __attribute__((amdgpu_waves_per_eu(BF16 && !BFS ? 4 : 1)))
 void step_kernel(DraftParams p) {
+  constexpr int kWaves = waves_of<D, NKT>(), kThreads = 64 * kWaves;
   constexpr int PIECES = BF16 ? 1 : 3;
   using SM = Smem<D, NKT, PIECES>;
   constexpr int KB = D / 32;                   // matrix instructions along the keys
@@ -520,6 +526,7 @@ void step_kernel(DraftParams p) {
   // The decays and Gram products of a tile with the tokens before it, in the matrix unit's layout: token i = 16 t + l16 a lane,
   // tokens j 4 qq + r of 16 jt.  From the tile's own end back to the first token: D_ij is the product of the decays on i's path
   // behind j, i's own among them: those behind in the lane's four, in the rows of lanes above, and in the tiles behind.
+  // With four waves, two of them each take every other tile of j.
   auto gram = [&](auto of_queries, int t) {
     constexpr bool Q = decltype(of_queries)::value;
     const int i = 16 * t + l16;
@@ -531,15 +538,18 @@ void step_kernel(DraftParams p) {
     const float own = Q ? 1.f : sm.beta[i] * sm.ks[i];
     float behind = 1.f;
     for (int jt = t; jt >= 0; --jt) {
+      const bool mine = kWaves == 2 || ((t - jt) & 1) == wave / 2;
       v4f acc = {0.f, 0.f, 0.f, 0.f};
+      if (mine) {
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        const v8bf kj = operand(&sm.k[16 * jt + l16][32 * kb]);
-        if constexpr (Q) {
+        for (int kb = 0; kb < KB; ++kb) {
+          const v8bf kj = operand(&sm.k[16 * jt + l16][32 * kb]);
+          if constexpr (Q) {
 #pragma unroll
-          for (int e = 0; e < PIECES; ++e) acc = mfma(kj, operand(&sm.q[16 * e + l16][32 * kb]), acc);
-        } else {
-          acc = mfma(kj, operand(&sm.k[16 * t + l16][32 * kb]), acc);
+            for (int e = 0; e < PIECES; ++e) acc = mfma(kj, operand(&sm.q[16 * e + l16][32 * kb]), acc);
+          } else {
+            acc = mfma(kj, operand(&sm.k[16 * t + l16][32 * kb]), acc);
+          }
         }
       }
       const int j = 16 * jt + 4 * qq;
@@ -562,10 +572,11 @@ void step_kernel(DraftParams p) {
       const float p[4] = {f321, f32_, f[3], 1.f};
       float (*to)[16] = Q ? sm.m.g.c : sm.m.g.a;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) to[j + r][l16] = on[r] ? above * p[r] * (own * ks[r]) * acc[r] : 0.f;
+      for (int r = 0; r < 4; ++r)
+        if (mine) to[j + r][l16] = on[r] ? above * p[r] * (own * ks[r]) * acc[r] : 0.f;
       behind *= g321 * bits_f32(rows[0]);
     }
-    if (!Q && qq == 0) sm.gamma[l16] = behind;
+    if (!Q && qq == 0 && wave == 0) sm.gamma[l16] = behind;
   };
   auto columns = [&](const float* row, float (&y)[SPW]) {
     if constexpr (SPW == 4) {
@@ -605,7 +616,7 @@ void step_kernel(DraftParams p) {
     if (!is8) project(std::false_type{}, &sm.k[16 * t][0], xk, xq);
     else if constexpr (HB != 4) project(std::true_type{}, &sm.k[16 * t][0], xk, xq);
     if constexpr (NKT == 1) __syncthreads();   // the scales have been read: the Gram products take their place
-    if (wave == 0) gram(std::false_type{}, t);
+    if (wave % 2 == 0) gram(std::false_type{}, t);
     else gram(std::true_type{}, t);
     __syncthreads();
 
@@ -673,6 +684,7 @@ void step_kernel(DraftParams p) {
 template <int D, int NKT, bool BF16>
 hipError_t launch(const DraftParams& p, int buf_kind, hipStream_t s) {
   const dim3 grid((unsigned)p.l.Hv, (unsigned)p.l.B);
+  constexpr int kThreads = 64 * waves_of<D, NKT>();
   const bool mixed = buf_kind == PACE_BUF_K4_VBF16;
   if (p.l.bf16_state) {                        // (int8 buffer only: checked by the caller)
     step_kernel<D, NKT, BF16, false, 4, 1, true><<<grid, kThreads, 0, s>>>(p);
