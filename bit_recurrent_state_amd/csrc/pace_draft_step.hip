@@ -633,18 +633,25 @@ void step_kernel(DraftParams p) {
     if (NKT > 1 && t > 0) add_tokens(16 * t, sm.m.g.a, -1.f, xk);
     // four tokens at a time: they are in the lanes of one row, which solve their triangle; what they add to those behind them
     // is one product a strip
+    float4 a0[4], a1[4];
+    float a23[4], w[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       const float (*a)[16] = sm.m.g.a + 16 * t + 4 * f;
-      const float4 a0 = *(const float4*)&a[0][4 * f], a1 = *(const float4*)&a[1][4 * f];
-      const float a23 = a[2][4 * f + 3];
+      a0[f] = *(const float4*)&a[0][4 * f];
+      a1[f] = *(const float4*)&a[1][4 * f];
+      a23[f] = a[2][4 * f + 3];
+      w[f] = -a[qq][l16];
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
       float y[4][SPW];
 #pragma unroll
       for (int s = 0; s < SPW; ++s) {
         y[0][s] = xk[s][0];
-        y[1][s] = xk[s][1] - a0.y * y[0][s];
-        y[2][s] = xk[s][2] - a0.z * y[0][s] - a1.z * y[1][s];
-        y[3][s] = xk[s][3] - a0.w * y[0][s] - a1.w * y[1][s] - a23 * y[2][s];
+        y[1][s] = xk[s][1] - a0[f].y * y[0][s];
+        y[2][s] = xk[s][2] - a0[f].z * y[0][s] - a1[f].z * y[1][s];
+        y[3][s] = xk[s][3] - a0[f].w * y[0][s] - a1[f].w * y[1][s] - a23[f] * y[2][s];
       }
       if (qq == f)
 #pragma unroll
@@ -655,11 +662,10 @@ void step_kernel(DraftParams p) {
         }
       wave_sync();
       if (f == 3) break;
-      const float w = -a[qq][l16];
       float u[SPW];
       columns(sm.u[16 * t + 4 * f + qq], u);
 #pragma unroll
-      for (int s = 0; s < SPW; ++s) xk[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(w, u[s], xk[s], 0, 0, 0);
+      for (int s = 0; s < SPW; ++s) xk[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[f], u[s], xk[s], 0, 0, 0);
     }
 
     // -------------------------------------------------------------- outputs
