@@ -313,6 +313,7 @@ void launch(const MoveParams& p, const Layout& y, hipStream_t s) {
     copy_kernel<W><<<dim3((unsigned)std::min(entries * p.Hkv, most), (unsigned)p.B), kCopyThreads, 0, s>>>(p, y, entries);
     return;
   }
+  // (1024 heads in 8 pieces of 1024 threads: 2^24 threads along x at most)
   const unsigned parts = (unsigned)(p.Hkv * 2 * (y.LB / W));
   // A workgroup's steps follow one another: 512 tokens each, 64 where that is all (the tokens of a draft).
   if (p.T <= 48)

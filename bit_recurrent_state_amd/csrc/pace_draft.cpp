@@ -11,8 +11,7 @@ using namespace pace;
 
 namespace {
 
-constexpr int64_t kMaxSpan = INT64_C(1) << 48;         // bytes from the first row to the last
-constexpr int64_t kMaxThreads = INT64_C(0xFFFFFFFF);   // of a launch
+constexpr int64_t kMaxSpan = INT64_C(1) << 48;   // bytes from the first row to the last
 
 int rounds_of(const pace_layer_cfg* c, int32_t most) { return (most + c->dP - 1) / c->dP; }
 

@@ -280,3 +280,26 @@ def test_moves_in_a_cache_of_more_than_2_to_32_bytes():
     pace.cache_read(cfg, cache, dst, at, out[2], out[3])
     for x, y in ((out[0], out[2]), (out[1], out[3])):
         assert torch.equal(x[0, ::2], y[0, : n // 2]) and torch.equal(x[1, : n - 38: 2], y[1, : n // 2 - 19])
+
+
+@pytest.mark.parametrize("with_nodes", [True, False])
+def test_moves_of_the_most_sequences(with_nodes):
+    """65535 sequences at once, against the same moves in two calls."""
+    pace = _lib()
+    Bn, H, T_, page = 65535, 32, 50, 16
+    halves = (slice(0, 30000), slice(30000, Bn))
+    cfg = lambda n: pace.CacheConfig(B=n, Hq=H, Hkv=H, d=64, num_pages=2 * Bn, max_pages=1, kind="int4", group=32, page=page)  # noqa: E731
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    cache = torch.randint(0, 256, (pace.cache_layout(cfg(Bn))["cache_bytes"],), generator=gen, device="cuda", dtype=torch.uint8)
+    tables = torch.randperm(2 * Bn, generator=gen, device="cuda").to(torch.int32).view(2, Bn, 1)
+    src, dst = tables[0], tables[0] if with_nodes else tables[1]
+    start = torch.randint(0, 6, (Bn,), generator=gen, device="cuda").to(torch.int32)
+    counts = torch.randint(0, T_, (Bn,), generator=gen, device="cuda").to(torch.int32)
+    nodes = (2 * torch.arange(T_, device="cuda", dtype=torch.int32)).expand(Bn, T_).contiguous() if with_nodes else None
+    want = cache.clone()
+    pace.cache_move(cfg(Bn), cache, src, dst, start, counts, nodes=nodes, most=T_)
+    assert not torch.equal(cache, want)
+    for h in halves:
+        n = h.stop - h.start
+        pace.cache_move(cfg(n), want, src[h], dst[h], start[h].clone(), counts[h].clone(), nodes=nodes[h] if with_nodes else None, most=T_)
+    assert torch.equal(cache, want)
