@@ -1,14 +1,15 @@
 """A small hybrid stack served through the library: gated-delta layers (pace_prefill_chunk,
-pace_decode_step) and one attention layer (pace_rotary, pace_cache_write, pace_cache_attention).
+pace_decode_step, pace_draft_step, pace_draft_commit) and one attention layer (pace_rotary,
+pace_cache_write, pace_cache_attention, pace_cache_move), drafts judged by pace_draft_verify.
 
     python examples/hybrid_decode.py
 
 1. A prompt goes through all layers at once: the delta layers in chunked prefill, the attention
    layer as a chain of drafted tokens over an empty cache.
 2. Tokens are decoded one by one: every layer's single-token form.
-3. A tree of drafted tokens is put to the attention layer.  The cache holds the drafts behind the
-   context; the best path is accepted, its keys and values are written again at their final
-   positions, and the delta layers then take the accepted tokens.
+3. A tree of drafted tokens goes through all layers: the delta layers give its outputs and stay as they
+   are, the cache holds its keys and values behind the context.  What is accepted stays on the device:
+   the delta layers take the accepted tokens, and the accepted entries move to their final positions.
 
 Weights and inputs are random (there is no model here); what is checked is that the forms agree:
 decoding token by token gives what one chunk gives, and every path of the tree what decoding that
@@ -23,7 +24,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import bit_recurrent_state_amd as pace  # noqa: E402
 
-B, WIDTH, HEADS, KV_HEADS, D, ROTARY, PAGE, MAX_PAGES = 2, 512, 8, 2, 128, 64, 64, 8
+B, WIDTH, HEADS, KV_HEADS, D, ROTARY, PAGE, MAX_PAGES, VOCABULARY = 2, 512, 8, 2, 128, 64, 64, 8, 8
 BF16 = torch.bfloat16
 
 
@@ -59,6 +60,19 @@ class DeltaLayer:
         return x + o.flatten(-2) @ self.out
 
 
+    def draft(self, x, tree):
+        """Outputs of drafts x [B, T, WIDTH]; their inputs are kept until some of them are accepted."""
+        q, k, v, a, b = self.inputs(x)
+        o = torch.empty_like(v)
+        pace.draft_step(self.cfg, self.state, self.buffer, q, k, v, a, b, o, tree=tree)
+        self.drafted = k, v, a, b
+        return x + o.flatten(-2) @ self.out
+
+    def commit(self, nodes, counts):
+        scratch = torch.empty(pace.draft_commit_workspace_bytes(self.cfg, nodes.shape[1]), dtype=torch.uint8, device="cuda")
+        pace.draft_commit(self.cfg, self.state, self.buffer, *self.drafted, nodes, counts, scratch)
+
+
 class AttentionLayer:
     """One attention layer over an 8-bit paged cache, half of every head rotated."""
 
@@ -90,7 +104,11 @@ class AttentionLayer:
         n = pace.cache_attention_workspace_bytes(self.cfg, T, longest)
         scratch = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
         pace.cache_attention(self.cfg, self.cache, self.table, q, lens, o, tree=tree, max_len=longest, workspace=scratch)
-        return x + o.flatten(-2) @ self.out, k, v
+        return x + o.flatten(-2) @ self.out
+
+    def keep(self, lens, nodes, counts):
+        """The accepted drafts' entries to their final places behind the context."""
+        pace.cache_move(self.cfg, self.cache, self.table, self.table, lens, counts, nodes=nodes)
 
 
 def weight(gen, n, m):
@@ -122,34 +140,60 @@ def main(prompt=150, steps=11):
         for layer in delta:
             z = layer.step(z)
         inputs.append(z)
-        outputs.append(attention.attend(z[:, None], lens, order[:1], order[:1])[0][:, 0])
+        outputs.append(attention.attend(z[:, None], lens, order[:1], order[:1])[:, 0])
         lens += 1
     back = lens - steps
-    chunk = attention.attend(torch.stack(inputs, 1), back, order[:steps], order[:steps])[0]
+    chunk = attention.attend(torch.stack(inputs, 1), back, order[:steps], order[:steps])
     found = {"token by token against one chunk": off(torch.stack(outputs, 1), chunk)}
 
     # 3. a tree of drafts behind the context: 0 -> (1 -> 3 -> 5, 2 -> 4)
     parents = [-1, 0, 0, 1, 2, 3]
     depth = torch.tensor([0, 1, 1, 2, 2, 3], device="cuda")
-    drafts = torch.randn((B, len(parents), WIDTH), generator=gen, device="cuda").to(BF16)
+    T = len(parents)
+    embedding, head = weight(gen, WIDTH, VOCABULARY).t().contiguous() * WIDTH ** 0.5, weight(gen, WIDTH, VOCABULARY)
+    tokens = torch.randint(VOCABULARY, (B, T), generator=gen, device="cuda").to(torch.int32)
+    drafts = embedding[tokens.long()]
     bits = torch.from_numpy(pace.tree_bits(parents))[None].cuda()
-    checked, k, v = attention.attend(drafts, lens, depth, order[: len(parents)], tree=bits)
+    before = [(layer.state.clone(), layer.buffer.clone()) for layer in delta]
+    through = [drafts]
+    for layer in delta:
+        through.append(layer.draft(through[-1], bits))
+    checked = attention.attend(through[-1], lens, depth, order[:T], tree=bits)
     for path in ([0, 2, 4], [0, 1, 3, 5]):
-        for i, node in enumerate(path):                 # decode the path alone, over the drafts' places
-            alone = attention.attend(drafts[:, node: node + 1], lens + i, order[:1], order[:1])[0]
-            name = f"tree against path {path}"
-            found[name] = max(found.get(name, 0.0), off(checked[:, node: node + 1], alone))
-    # the longer path is accepted: its keys and values move to their final places, the others' are
-    # left behind the new end, and the delta layers take its tokens
-    final = torch.tensor([path.index(i) if i in path else -1 for i in range(len(parents))], device="cuda")
-    at = torch.where(final >= 0, lens[:, None] + final, -1).to(torch.int32)
-    pace.cache_write(attention.cfg, attention.cache, attention.table, at, k, v)
-    for node in path:
-        z = drafts[:, node]
-        for layer in delta:
-            z = layer.step(z)
-    lens += len(path)
+        name = f"tree against path {path}"
+        found[name] = 0.0
+        for layer, x, y in zip(delta, through, through[1:]):   # decode the path alone, in a copy of the layer
+            kept = layer.state, layer.buffer
+            layer.state, layer.buffer = layer.state.clone(), layer.buffer.clone()
+            for node in path:
+                found[name] = max(found[name], off(y[:, node], layer.step(x[:, node])))
+            layer.state, layer.buffer = kept
+        for i, node in enumerate(path):                 # (before the drafts are written again, over their places)
+            alone = attention.attend(through[-1][:, node: node + 1], lens + i, order[:1], order[:1])
+            found[name] = max(found[name], off(checked[:, node: node + 1], alone))
+    assert all(torch.equal(a, layer.state) and torch.equal(b, layer.buffer) for (a, b), layer in zip(before, delta))
+
+    # the drafts' entries as they were, the accepted path, and what every layer keeps of it
+    checked = attention.attend(through[-1], lens, depth, order[:T], tree=bits)
+    target = torch.softmax((checked @ head).float(), dim=-1)
+    judge = pace.VerifyConfig(B=B, T=T, V=VOCABULARY)
+    nodes = torch.empty((B, T), dtype=torch.int32, device="cuda")
+    counts, following = torch.empty((2, B), dtype=torch.int32, device="cuda")
+    scratch = torch.empty(pace.draft_verify_workspace_bytes(judge), dtype=torch.uint8, device="cuda")
+    pace.draft_verify(judge, target, tokens, torch.tensor([parents], dtype=torch.int32, device="cuda"),
+                      torch.rand((B, T), generator=gen, device="cuda"), nodes, counts, following, workspace=scratch)
+    for layer in delta:
+        layer.commit(nodes, counts)
+    attention.keep(lens, nodes, counts)
+    lens += counts
+
+    # the next step begins with the token that follows
+    z = embedding[following.long()]
+    for layer in delta:
+        z = layer.step(z)
+    attention.attend(z[:, None], lens, order[:1], order[:1])
     torch.cuda.synchronize()
+    print(f"accepted drafts {counts.tolist()}, then tokens {following.tolist()}")
     for name, value in found.items():
         print(f"{name}: largest difference {value:.2e} of the largest value")
     return found
