@@ -597,9 +597,11 @@ void step_kernel(DraftParams p) {
         columns(sm.u[j0 + 4 * f + qq], u[f]);
       }
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
+      for (int f = 0; f < 4; ++f) {
+        if (j0 + 4 * f >= end) break;
 #pragma unroll
         for (int s = 0; s < SPW; ++s) x[s] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[f], u[f][s], x[s], 0, 0, 0);
+      }
     }
   };
 
@@ -661,7 +663,7 @@ void step_kernel(DraftParams p) {
           else *(float2*)row = make_float2(y[r][0], y[r][1]);
         }
       wave_sync();
-      if (f == 3) break;
+      if (f == 3 || 16 * t + 4 * f + 4 >= N) break;      // (zeros from there on, and nobody asks for them)
       float u[SPW];
       columns(sm.u[16 * t + 4 * f + qq], u);
 #pragma unroll
