@@ -315,8 +315,10 @@ void launch(const MoveParams& p, const Layout& y, hipStream_t s) {
   }
   // (1024 heads in 8 pieces of 1024 threads: 2^24 threads along x at most)
   const unsigned parts = (unsigned)(p.Hkv * 2 * (y.LB / W));
-  // A workgroup's steps follow one another: 512 tokens each, 64 where that is all (the tokens of a draft).
-  if (p.T <= 48)
+  // A workgroup's steps follow one another: 64 tokens each, or 512 where there are too few workgroups to fill the
+  // chip with the small ones.  int8, 8 heads of 128, half of T kept, the small and the large: 4 x 16384 150 and 45.6 us, 4 x 300
+  // 7.6 and 3.8, 8 x 8192 84 and 48, 16 x 8192 105 and 94, 64 x 1000 47.5 and 65.9, 64 x 300 19.3 and 44.
+  if (p.T <= 64 || (int64_t)parts * p.B > 256)
     move_kernel<W, 256, 1><<<dim3(parts, (unsigned)p.B), 256, 0, s>>>(p, y);
   else
     move_kernel<W, 1024, 2><<<dim3(2 * parts, (unsigned)p.B), 1024, 0, s>>>(p, y);

@@ -428,12 +428,16 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(VerifyParams p) {
 
 template <typename E, int NODES>
 void launch(const VerifyParams& p, hipStream_t s) {
-  // Workgroups a sequence, so that about four a compute unit read the rows.
-  const int slices = std::min(1024 / p.B, (p.chunks + kSumThreads / 64 - 1) / (kSumThreads / 64));
-  if (p.chunks <= kWaves || slices < 2) {
+  // Two kernels where one workgroup a sequence leaves much of the chip idle for long: few sequences, long rows.  Chains of 8,
+  // drawn, fp32, in one kernel and in two: V = 131072: 1 sequence 21.5 and 8.1 us, 64 28.3 and 18.9, 128 35.3 and
+  // 31.5, 192 45.0 and 47.8; V = 32768: 1 sequence 9.4 and 8.0, 32 10.2 and 10.4, 128 12.6 and 14.3; V = 16384: 1 sequence
+  // 7.8 and 8.0.
+  if (p.chunks <= kWaves / 2 || p.B > std::min(2 * p.chunks, 128)) {
     verify_kernel<E, NODES><<<p.B, kThreads, 0, s>>>(p);
     return;
   }
+  // (about four workgroups a compute unit read the rows)
+  const int slices = std::min(1024 / p.B, (p.chunks + kSumThreads / 64 - 1) / (kSumThreads / 64));
   sums_kernel<E, NODES><<<dim3((unsigned)slices, (unsigned)p.B), kSumThreads, 0, s>>>(p);
   finish_kernel<E, NODES><<<p.B, kThreads, 0, s>>>(p);
 }
@@ -441,6 +445,7 @@ void launch(const VerifyParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_draft_verify(const VerifyParams& p, int prob_bf16, hipStream_t stream) {
+  // (LDS for 64 nodes or for 1024: 64 chains of 8 over 131072 tokens 18.8 us, with the larger 22.2)
   if (p.T <= 64) {
     if (prob_bf16) launch<uint16_t, 64>(p, stream);
     else launch<float, 64>(p, stream);

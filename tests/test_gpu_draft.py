@@ -404,6 +404,19 @@ def test_accepted_paths_and_kept_entries_move_in_place(kind, d, group, page, T):
 
 
 @pytest.mark.parametrize("kind,d,group,page", KINDS)
+@pytest.mark.parametrize("T", [65, 200])
+def test_kept_entries_of_many_sequences_move_in_place(kind, d, group, page, T):
+    """As many (sequence, head) pairs as the kernel of small steps takes, several steps each."""
+    rng, B = np.random.default_rng(T + 7), 34
+    s = Cached(T + 7, B, 4, d, kind, group, page, MP=-(-(T + 40) // page))
+    nodes, counts = np.full((B, T), -1, dtype=np.int32), np.zeros(B, dtype=np.int32)
+    for b in range(B):
+        counts[b] = rng.integers(0, T + 1)
+        nodes[b, : counts[b]] = np.sort(rng.choice(T, counts[b], replace=False))
+    s.check(rng.integers(0, 40, B), nodes, counts)
+
+
+@pytest.mark.parametrize("kind,d,group,page", KINDS)
 @pytest.mark.parametrize("T", [1, 63, 257])
 def test_forks_copy_into_other_pages(kind, d, group, page, T):
     B = 3
