@@ -15,6 +15,12 @@
 //                sums.  One scale a (column, 32 keys).
 //   solve        16 tokens at a time in the matrix unit's layout (4 tokens x 4 columns a lane), four at a time within them
 // Queries enter as they are in bf16, as three bf16 pieces (exact) in fp32.  Everything else is fp32.
+//
+// Measured (graph), 32/16 heads of 128, int4 state: 64 chains of up to 8 14.5 us, 2.1 TB/s (a large copy: 5.1).  All 2048
+// workgroups are on the chip at once and last 5.9 to 14 us: the vector unit issues half of the time, the matrix unit 22%, and
+// waves wait for their turn 46% of theirs.  16 trees of up to 25 (mixed heads and buffer): 13.8 us, two workgroups a
+// compute unit, vector unit 40%: latency of one tile after another.  One sequence's five tokens: 5.7 us, a workgroup's
+// chain of loads, tokens, projections, Gram, solve, outputs 4.6 of them.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -27,7 +33,8 @@ namespace pace {
 namespace {
 
 // Waves of a workgroup: two where one tile holds all tokens (eight such workgroups a compute unit), four beyond it
-// (LDS leaves four, or fewer).
+// (LDS leaves four, or fewer).  64 chains of 8 in two waves 15.2 us, in four 17.0 (one sequence's five: 6.0 and 5.4); 16 trees
+// of 25 in two 17.8 us, in four 14.1.
 template <int D, int NKT>
 constexpr int waves_of() {
   return NKT == 1 || D == 64 ? 2 : 4;
@@ -697,8 +704,8 @@ hipError_t launch(const DraftParams& p, int buf_kind, hipStream_t s) {
   if (p.l.bf16_state) {                        // (int8 buffer only: checked by the caller)
     step_kernel<D, NKT, BF16, false, 4, 1, true><<<grid, kThreads, 0, s>>>(p);
   } else if (BF16 && p.l.mask8 == 0 && !mixed && p.l.group == 64) {
-    // All heads in 4 bits, the symmetric layout's groups: 16 registers fewer, no second way through the projections, half
-    // as many scalings.  64 x 8 drafts: 15.5 us, by the general kernel 16.1; one sequence's five: 6.4 and 6.8.
+    // All heads in 4 bits, the symmetric layout's groups: fewer registers, no second way through the projections, half
+    // as many scalings.  When it was added, 64 x 8 drafts took 15.5 us, by the general kernel 16.1; one sequence's five 6.4 and 6.8.
     if constexpr (BF16) step_kernel<D, NKT, true, false, 4, 2, false><<<grid, kThreads, 0, s>>>(p);
   } else if (mixed) {
     step_kernel<D, NKT, BF16, true, 0, 1, false><<<grid, kThreads, 0, s>>>(p);
@@ -710,6 +717,7 @@ hipError_t launch(const DraftParams& p, int buf_kind, hipStream_t s) {
 
 template <int D, bool BF16>
 hipError_t by_tiles(const DraftParams& p, int buf_kind, hipStream_t s) {
+  // (LDS goes by the tiles: 64 chains of 8 in the one tile that they need 14.8 us, in the kernel for two 17.9)
   const int t = draft_tiles(p.l.dP, p.T);
   if (t <= 1) return launch<D, 1, BF16>(p, buf_kind, s);
   if (t <= 2) return launch<D, 2, BF16>(p, buf_kind, s);

@@ -7,6 +7,10 @@
 // token.  It is summed in chunks of 2048 tokens, one a wave; the token is found by the chunks' sums and then inside its
 // chunk.  All in fp64: the fp32 (bf16) inputs are exact, and a sum of 2^24 of them is off by 2^-29 of a step of fp32.
 //
+// Bound by memory for large batches and by latency for small ones.  Measured (graph): 64 chains of 8 over 131072 tokens,
+// fp32, drawn: 18.9 us, of which the sums 14.8 (4.5 TB/s; a large copy 5.1) and the rest 4.2; 16 trees of 25 over
+// 100003 tokens, bf16, not drawn: 10.9 us (7.5 and 4.4): parents -> probabilities -> walk -> row; one chain of 5: 8.0 us.
+//
 // Few sequences over a large vocabulary: the first row that is asked for is summed by several workgroups a sequence, each
 // of which walks there by itself; a second kernel goes on from there.  Otherwise one workgroup a sequence does it all.
 #include <hip/hip_runtime.h>
