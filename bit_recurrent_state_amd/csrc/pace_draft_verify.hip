@@ -9,7 +9,8 @@
 //
 // Bound by memory for large batches and by latency for small ones.  Measured (graph): 64 chains of 8 over 131072 tokens,
 // fp32, drawn: 18.9 us, of which the sums 14.8 (4.5 TB/s; a large copy 5.1) and the rest 4.2; 16 trees of 25 over
-// 100003 tokens, bf16, not drawn: 10.9 us (7.5 and 4.4): parents -> probabilities -> walk -> row; one chain of 5: 8.0 us.
+// 100003 tokens, bf16, not drawn: 10.9 us (7.5 and 4.4): parents -> probabilities -> walk -> row; one chain of 5 over
+// 32768: 9.5 us.
 //
 // Few sequences over a large vocabulary: the first row that is asked for is summed by several workgroups a sequence, each
 // of which walks there by itself; a second kernel goes on from there.  Otherwise one workgroup a sequence does it all.
@@ -432,11 +433,11 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(VerifyParams p) {
 
 template <typename E, int NODES>
 void launch(const VerifyParams& p, hipStream_t s) {
-  // Two kernels where one workgroup a sequence leaves much of the chip idle for long: few sequences, long rows.  Chains of 8,
-  // drawn, fp32, in one kernel and in two: V = 131072: 1 sequence 21.5 and 8.1 us, 64 28.3 and 18.9, 128 35.3 and
-  // 31.5, 192 45.0 and 47.8; V = 32768: 1 sequence 9.4 and 8.0, 32 10.2 and 10.4, 128 12.6 and 14.3; V = 16384: 1 sequence
-  // 7.8 and 8.0.
-  if (p.chunks <= kWaves / 2 || p.B > std::min(2 * p.chunks, 128)) {
+  // Two kernels where one workgroup a sequence leaves much of the chip idle for long: few sequences, rows of more than a chunk a
+  // wave.  Chains of 8, drawn, fp32, in one kernel and in two: V = 131072: 1 sequence 21.5 and 8.1 us, 64 28.3 and 18.9, 128
+  // 35.3 and 31.5, 192 45.0 and 47.8; V = 65536: 16 14.5 and 10.4, 256 28.3 and 30.7; V = 32768: 1 sequence 9.4 and 8.0 in a
+  // graph, but 9.4 and 11.6 called eagerly (a second launch), 32 10.2 and 10.4, 128 12.6 and 14.3.
+  if (p.chunks <= kWaves || p.B > std::min(2 * p.chunks, 128)) {
     verify_kernel<E, NODES><<<p.B, kThreads, 0, s>>>(p);
     return;
   }
