@@ -7,7 +7,7 @@
 // ahead of those.  Keys move as whole pieces; values are put together from the bytes of four tokens.
 // Measured (graph): half of 4 x 16384 entries, int8, 8 heads of 128: 45.4 us, 2.6 TB/s of entries; those kept lie among those
 // dropped, so that nearly every line of the old contexts is read, 3.8 TB/s of lines (a large copy: 5.1).  Waves wait for
-// memory 60% of their time: one workgroup a compute unit, a step in flight.  64 accepted paths of 25: 6.0 us, latency of
+// memory 60% of their time; a second step in flight made it no faster (46 us).  64 accepted paths of 25: 6.0 us, latency of
 // counts -> nodes -> pages -> entries.
 // Without nodes nothing shifts: pages are copied record by record, all at once, and the tokens of the first and
 // last page that are not asked for are left out by masks.  8 forks of 4093 tokens, int4: 11.4 us, 3.7 TB/s.

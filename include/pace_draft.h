@@ -111,7 +111,7 @@ typedef struct {
  * target_stride, draft_stride: elements from one row to the next (>= V; row b * T + i), so that rows may be padded.
  * Out: nodes int32 [B][T]: the accepted path from node 0, then -1; counts int32 [B]: its length (0 where draft_lens is
  * 0); next int32 [B] (-1 there).
- * workspace: pace_draft_verify_workspace_bytes(cfg) bytes, 256-byte aligned (NULL if 0).
+ * workspace: pace_draft_verify_workspace_bytes(cfg) bytes, 256-byte aligned.
  * A result repeats bit for bit and does not depend on the other sequences.
  * Errors: PACE_EINVAL for null pointers, sizes below 1, bad strides, a workspace that is too small, misalignment (elements');
  * PACE_EUNSUPPORTED for sizes over those above, or rows that span more than 2^48 bytes. */
@@ -122,7 +122,7 @@ pace_status pace_draft_verify(const pace_verify_cfg* cfg, const void* target, in
                               int32_t* counts, int32_t* next, void* workspace,
                               size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of pace_draft_verify, written to *bytes_out (0: none needed).  Host only.
+/* Workspace bytes of pace_draft_verify, written to *bytes_out.  Host only.
  * Errors (nothing is written) as pace_draft_verify. */
 pace_status pace_draft_verify_workspace_bytes(const pace_verify_cfg* cfg, size_t* bytes_out);
 
@@ -137,10 +137,11 @@ pace_status pace_draft_verify_workspace_bytes(const pace_verify_cfg* cfg, size_t
  * start, counts int32 [B], nodes int32 (device; nodes_stride in elements, rows of T or more); tables int32 [B][max_pages], as pace_cache.h's.
  * counts are taken as 0 below 0, as T above it.  An entry whose position, here or there, is negative, past the
  * table, or in a page that is not there, is left out: what lies at its destination stays.
- * Within a sequence entries move as if all were read before any is written, provided that nodes[0] < nodes[1] < ..., with
- * nodes[i] >= i (entries with a negative node are left out); where the two tables share no page, nodes may be any.  No page that one sequence's entries are written to may be
- * read or written for another sequence in the same call (with one exception: a page may be read by any number of them
- * where none writes it); shared pages are copied first.
+ * Within a sequence entries move as if all were read before any is written, provided that a page which both tables hold
+ * stands at the same entry of both (one table; a prefix that a fork keeps), and nodes[0] < nodes[1] < ..., with
+ * nodes[i] >= i (entries with a negative node are left out); where the two tables share no page, nodes may be any.
+ * No page that one sequence's entries are written to may be read or written for another sequence in the same call; pages
+ * that are only read may be any number of sequences'.  (Shared pages are copied first.)
  * cfg's Hq and io_dtype have no part in it.  T: upper bound of the counts (host).  T == 0 is allowed and does nothing.
  * Errors: PACE_EINVAL for null pointers, T < 0, nodes_stride < T where nodes is given, misalignment (cache: 256 bytes); PACE_EUNSUPPORTED
  * as pace_cache_write, and for T over 2^30. */

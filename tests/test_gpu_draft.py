@@ -427,6 +427,19 @@ def test_forks_copy_into_other_pages(kind, d, group, page, T):
     s.check([5, 0, 1], nodes, [T, T, T - 1], src=src, dst=s.other)
 
 
+@pytest.mark.parametrize("kind,d,group,page", KINDS)
+def test_forks_that_keep_a_prefix(kind, d, group, page):
+    """Tables that hold the same pages at their first entries: what lies there stays, or moves in place."""
+    T = 2 * page + 21
+    s = Cached(23, 1, 2, d, kind, group, page, MP=4)
+    dst = s.other.copy()
+    dst[:, :2] = s.src[:, :2]
+    s.check([0], None, [T], dst=dst, most=T)
+    s.check([3], None, [T - 9], dst=dst, most=T)
+    nodes = np.sort(np.random.default_rng(page).choice(T, T // 2, replace=False))[None]
+    s.check([2], nodes, [T // 2], dst=dst)
+
+
 def test_moves_leave_out_what_is_not_there():
     s = Cached(3, 3, 2, 64, "int8", 32, 16, MP=6)
     T = 50
