@@ -205,6 +205,23 @@ void step_kernel(DraftParams p) {
   const int bits = BFS ? 16 : is8 ? 8 : 4;
   const uint64_t below = HB != 4 && h ? (l.mask8 & ((1ull << h) - 1ull)) : 0ull;
   const uint8_t* rec = l.state + (uint64_t)b * l.seq_stride + (uint64_t)h * l.rec4 + (uint64_t)__popcll(below) * (l.rec8 - l.rec4);
+  // a thread's column of scales and zero points (groups of 32 keys, or 64); ahead of the
+  // state, as they are waited for with the tokens
+  const int wide = l.group == 64;
+  uint16_t column_s[KB];
+  uint8_t column_z[KB];
+  const int column = min(tid, D - 1);
+  if constexpr (!BFS) {
+    const int NG = KB >> wide;
+    const uint16_t* scales = (const uint16_t*)(rec + (is8 ? l.scales_off8 : l.scales_off4));
+    const uint8_t* zeros = rec + (is8 ? l.zeros_off8 : l.zeros_off4);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const int i = column * NG + (kb >> wide);
+      column_s[kb] = scales[i];
+      if (asym) column_z[kb] = zeros[is8 ? i : i >> 1];
+    }
+  }
   // a lane's columns: c0 .. c0 + SPW - 1, one a strip; their codes of keys 8 qq .. + 7 of every 32 (one unit each)
   const int c0 = wave * CW + SPW * l16;
   constexpr int AW = BFS ? 4 * KB : HB == 4 ? KB : 2 * KB;
@@ -234,23 +251,6 @@ void step_kernel(DraftParams p) {
       raw[s][0] = v.x; raw[s][1] = v.y;
     }
   }
-  // a thread's column of scales and zero points (groups of 32 keys, or 64)
-  const int wide = l.group == 64;
-  uint16_t column_s[KB];
-  uint8_t column_z[KB];
-  const int column = min(tid, D - 1);
-  if constexpr (!BFS) {
-    const int NG = KB >> wide;
-    const uint16_t* scales = (const uint16_t*)(rec + (is8 ? l.scales_off8 : l.scales_off4));
-    const uint8_t* zeros = rec + (is8 ? l.zeros_off8 : l.zeros_off4);
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      const int i = column * NG + (kb >> wide);
-      column_s[kb] = scales[i];
-      if (asym) column_z[kb] = zeros[is8 ? i : i >> 1];
-    }
-  }
-
   // ----------------------------------------------------------------- tokens
   const int len = __builtin_amdgcn_readfirstlane(min(max(len_raw, 0), T));
   const int n = __builtin_amdgcn_readfirstlane(min(max(count, 0), l.dP - 1)), N = n + len;
