@@ -50,8 +50,8 @@ __device__ inline v8bf as_operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d
   return __builtin_bit_cast(v8bf, w);
 }
 
-// NKT: 16-token tiles of the buffered and drafted tokens.  PIECES: of a query.
-template <int D, int NKT, int PIECES>
+// NKT: 16-token tiles of the buffered and drafted tokens.  PIECES: of a query.  KPS: 32-key blocks that share a scale.
+template <int D, int NKT, int PIECES, int KPS>
 struct alignas(16) Smem {
   static constexpr int NK = 16 * NKT;
   static constexpr int TS = D + 8;              // row stride of tokens (bf16): 16 rows on distinct banks
@@ -62,12 +62,13 @@ struct alignas(16) Smem {
     alignas(16) float a[NK][16];                // [j][i]: beta_i D_ij (k_j . k_i), 0 for j >= i
     alignas(16) float c[NK][16];                // [j][i]: D_ij (k_j . q_i)
   };
-  struct Scales {                               // of (32 keys, column), bf16
-    alignas(16) uint16_t s[D / 32][D];
-    alignas(16) uint16_t z[D / 32][D];          // minus what the operand's codes are too large by
+  struct Scales {                               // of (32 keys, or 64, column), bf16
+    alignas(16) uint16_t s[D / 32 / KPS][D];
+    alignas(16) uint16_t z[D / 32 / KPS][D];    // minus what the operand's codes are too large by
   };
-  // A tile is projected before its Gram products are formed, so both fit one place where there is one tile (eight
-  // workgroups a compute unit at D = 128); with more the scales are needed to the end.
+  // The Gram products are formed first, while the state is on its way.  With one tile and 32-key blocks that would leave
+  // room for seven workgroups a compute unit at D = 128, not eight: there the tile is projected first, and both use one place.
+  static constexpr bool kGramFirst = NKT > 1 || KPS > 1;
   struct Both {
     Gram g;
     Scales s;
@@ -76,7 +77,7 @@ struct alignas(16) Smem {
     Gram g;
     Scales s;
   };
-  alignas(16) std::conditional_t<NKT == 1, Either, Both> m;
+  alignas(16) std::conditional_t<kGramFirst, Both, Either> m;
   alignas(16) float ks[NK], decay[NK], beta[NK], gamma[16];
   uint64_t row[NK < kMaxDrafts ? NK : kMaxDrafts];   // tree bits
 };
@@ -101,7 +102,7 @@ __global__ __launch_bounds__((64 * waves_of<D, NKT>())) __attribute__((amdgpu_wa
 void step_kernel(DraftParams p) {
   constexpr int kWaves = waves_of<D, NKT>(), kThreads = 64 * kWaves;
   constexpr int PIECES = BF16 ? 1 : 3;
-  using SM = Smem<D, NKT, PIECES>;
+  using SM = Smem<D, NKT, PIECES, KPS>;
   constexpr int KB = D / 32;                   // matrix instructions along the keys
   constexpr int SPW = D / 16 / kWaves;         // 16-column strips a wave
   constexpr int CW = D / kWaves;               // columns a wave
@@ -208,16 +209,16 @@ void step_kernel(DraftParams p) {
   // a thread's column of scales and zero points (groups of 32 keys, or 64); ahead of the
   // state, as they are waited for with the tokens
   const int wide = l.group == 64;
-  uint16_t column_s[KB];
-  uint8_t column_z[KB];
+  uint16_t column_s[KB / KPS];
+  uint8_t column_z[KB / KPS];
   const int column = min(tid, D - 1);
   if constexpr (!BFS) {
-    const int NG = KB >> wide;
+    const int NG = KPS > 1 ? KB / KPS : KB >> wide;
     const uint16_t* scales = (const uint16_t*)(rec + (is8 ? l.scales_off8 : l.scales_off4));
     const uint8_t* zeros = rec + (is8 ? l.zeros_off8 : l.zeros_off4);
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      const int i = column * NG + (kb >> wide);
+    for (int kb = 0; kb < KB / KPS; ++kb) {
+      const int i = column * NG + (KPS > 1 ? kb : kb >> wide);
       column_s[kb] = scales[i];
       if (asym) column_z[kb] = zeros[is8 ? i : i >> 1];
     }
@@ -395,9 +396,9 @@ void step_kernel(DraftParams p) {
   if constexpr (!BFS) {
     if (tid < D) {
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int kb = 0; kb < KB / KPS; ++kb) {
         sm.m.s.s[kb][tid] = column_s[kb];
-        const int odd = (tid * (KB >> wide) + (kb >> wide)) & 1;   // (4 bits: two zero points a byte)
+        const int odd = (KPS > 1 ? tid * (KB / KPS) + kb : tid * (KB >> wide) + (kb >> wide)) & 1;   // (4 bits: two zero points a byte)
         const int zp = is8 ? column_z[kb] : (column_z[kb] >> (4 * odd)) & 15;
         const float z = asym ? (float)zp : (float)(1 << (bits - 1));
         sm.m.s.z[kb][tid] = (uint16_t)two_bf16(-((is8 ? 0.f : 16.f) + z), 0.f);
@@ -457,7 +458,7 @@ void step_kernel(DraftParams p) {
         sum_k = qq == kb ? k : sum_k;
         sum_q = qq == kb ? acc[0] : sum_q;
       }
-      const int kb = KB == 4 ? qq : qq & 1;    // (two blocks: the sums of the others are zeros)
+      const int kb = (KB == 4 ? qq : qq & 1) / KPS;      // (two blocks: the sums of the others are zeros)
 #pragma unroll
       for (int s = 0; s < SPW; s += 2) {
         const uint32_t sc = *(const uint32_t*)&sm.m.s.s[kb][c0 + s], zp = *(const uint32_t*)&sm.m.s.z[kb][c0 + s];
@@ -503,7 +504,7 @@ void step_kernel(DraftParams p) {
       for (int s = s0; s < s0 + 2; ++s)
 #pragma unroll
         for (int i = 0; i < (E8 ? 2 : 1) * KPS; ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb0 + i : kb0 + i]));
-      sc[turn & 1] = *(const uint32_t*)&sm.m.s.s[kb0][c0 + s0];
+      sc[turn & 1] = *(const uint32_t*)&sm.m.s.s[kb0 / KPS][c0 + s0];
 #pragma unroll
       for (int kb = kb0; kb < kb0 + KPS; ++kb)
 #pragma unroll
@@ -621,12 +622,18 @@ void step_kernel(DraftParams p) {
         __syncthreads();
       }
     }
+    auto grams = [&] {
+      if (wave % 2 == 0) gram(std::false_type{}, t);
+      else gram(std::true_type{}, t);
+    };
+    if constexpr (SM::kGramFirst) grams();
     v4f xk[SPW], xq[SPW];
     if (!is8) project(std::false_type{}, &sm.k[16 * t][0], xk, xq);
     else if constexpr (HB != 4) project(std::true_type{}, &sm.k[16 * t][0], xk, xq);
-    if constexpr (NKT == 1) __syncthreads();   // the scales have been read: the Gram products take their place
-    if (wave % 2 == 0) gram(std::false_type{}, t);
-    else gram(std::true_type{}, t);
+    if constexpr (!SM::kGramFirst) {
+      __syncthreads();                         // the scales have been read: the Gram products take their place
+      grams();
+    }
     __syncthreads();
 
     // ---------------------------------------------------------------- solve
