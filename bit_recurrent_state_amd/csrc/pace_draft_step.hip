@@ -16,11 +16,12 @@
 //   solve        16 tokens at a time in the matrix unit's layout (4 tokens x 4 columns a lane), four at a time within them
 // Queries enter as they are in bf16, as three bf16 pieces (exact) in fp32.  Everything else is fp32.
 //
-// Measured (graph), 32/16 heads of 128, int4 state: 64 chains of up to 8 14.5 us, 2.1 TB/s (a large copy: 5.1).  All 2048
-// workgroups are on the chip at once and last 5.9 to 14 us: the vector unit issues half of the time, the matrix unit 22%, and
-// waves wait for their turn 46% of theirs.  16 trees of up to 25 (mixed heads and buffer): 13.8 us, two workgroups a
-// compute unit, vector unit 40%: latency of one tile after another.  One sequence's five tokens: 5.7 us, a workgroup's
-// chain of loads, tokens, projections, Gram, solve, outputs 4.6 of them.
+// Measured (graph), 32/16 heads of 128, int4 state: 64 chains of up to 8 14.15 us, 2.1 TB/s (a large copy: 5.1).  All 2048
+// workgroups are on the chip at once: their loads take 6 us together, so that the last quarter waits for its tokens, and
+// then takes the 6 us of a workgroup; vector unit and LDS are busy half of the time each, the matrix unit 23%, waves wait for
+// their turn 44% of theirs.  16 trees of up to 25 (mixed heads and buffer): 13.3 us, two workgroups a compute unit, vector
+// unit 42%: latency of one tile after another.  One sequence's five tokens: 5.6 us, a workgroup's chain of loads, tokens,
+// Gram, projections, solve, outputs 4.6 of them.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
