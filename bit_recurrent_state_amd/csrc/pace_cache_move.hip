@@ -76,7 +76,7 @@ __device__ inline void walk(const MoveParams& p, const Layout& y, int piece, int
   const int count = min(max(p.counts[b], 0), p.T);
   const int64_t end = min(start + count, (int64_t)p.max_pages << p.page_shift);
   const int64_t base = max(start, (int64_t)0) & ~(int64_t)15;
-  if (base >= end) return;
+  if (max(start, (int64_t)0) >= end) return;   // (from here on count > 0: there is a node to read)
   const int steps = (int)((end - base + STEP - 1) / STEP);
   const int32_t* const nodes = p.nodes + b * p.nodes_stride;
   const int32_t* const src_table = p.src_table + (int64_t)b * p.max_pages;
@@ -317,7 +317,7 @@ void launch(const MoveParams& p, const Layout& y, hipStream_t s) {
     copy_kernel<W><<<dim3((unsigned)std::min(entries * p.Hkv, most), (unsigned)p.B), kCopyThreads, 0, s>>>(p, y, entries);
     return;
   }
-  // (1024 heads in 8 pieces of 1024 threads: 2^24 threads along x at most)
+  // (1024 heads in 16 parts of 1024 threads: 2^24 threads along x at most)
   const unsigned parts = (unsigned)(p.Hkv * 2 * (y.LB / W));
   // A workgroup's steps follow one another: 64 tokens each, or 512 where there are too few workgroups to fill the
   // chip with the small ones.  int8, 8 heads of 128, half of T kept, the small and the large: 4 x 16384 150 and 45.6 us, 4 x 300

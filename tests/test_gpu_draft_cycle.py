@@ -303,3 +303,17 @@ def test_moves_of_the_most_sequences(with_nodes):
         n = h.stop - h.start
         pace.cache_move(cfg(n), want, src[h], dst[h], start[h].clone(), counts[h].clone(), nodes=nodes[h] if with_nodes else None, most=T_)
     assert torch.equal(cache, want)
+
+
+def test_moves_of_nothing_read_no_nodes():
+    """Sequences without entries to move, whose start lies inside a tile: rows of nodes next to what they may not be taken
+    for, and caches as they were."""
+    pace = _lib()
+    for start in (0, 5, 15, 16, 37):
+        cfg = pace.CacheConfig(B=2, Hq=2, Hkv=2, d=64, num_pages=8, max_pages=4, kind="int8", group=64, page=16)
+        cache = torch.randint(0, 256, (pace.cache_layout(cfg)["cache_bytes"],), device="cuda", dtype=torch.uint8)
+        want, table = cache.clone(), dev(np.array([[7, 1, 3, 0], [2, 6, 4, 5]], dtype=np.int32))
+        nodes = torch.arange(3, 23, device="cuda", dtype=torch.int32).view(2, 10)
+        for counts in ([0, 0], [-3, 0], [0, -2 ** 31]):
+            pace.cache_move(cfg, cache, table, table, dev(np.array([start, start], dtype=np.int32)), dev(np.array(counts, dtype=np.int32)), nodes=nodes)
+            assert torch.equal(cache, want)
