@@ -40,6 +40,7 @@ LAYERS = {
     "asym_g64_dP32": (2, 6, 2, 128, 64, "asym", "int8", True, 32, [4, 8, 4, 4, 8, 4]),
     "sym8_dP16": (2, 4, 2, 128, 64, "sym", "int8", True, 16, [8, 8, 4, 8]),
     "d64_g64_dP1": (2, 3, 1, 64, 64, "sym", "int8", True, 1, None),
+    "asym4_g64": (2, 8, 4, 128, 64, "asym", "int8", True, 8, None),
     "f32_g32_mixed_dP32": (2, 2, 1, 128, 32, "sym", "mixed", False, 32, None),
     "bf16_state": (2, 8, 4, 128, 32, "bf16", "int8", True, 8, None),
     "bf16_state_f32_d64": (2, 4, 2, 64, 32, "bf16", "int8", False, 12, None),
