@@ -255,12 +255,15 @@ __device__ inline void token_at(const VerifyParams& p, const Row<E>& row, const 
     __syncthreads();
     return;
   }
-  double r = u * total, before = 0.0, found = 0.0;
+  // (no sum exceeds all of the total, but one that is formed in another order may)
+  double r = u < 1.0 ? u * total : HUGE_VAL, before = 0.0, found = 0.0;
   int chunk = -1, last = 0;
   for (int i = 0; i < p.chunks && chunk < 0; i += 64) {
     const double t = i + lane < p.chunks ? sums[i + lane] : 0.0;
     const double upto = before + wave_scan(t);
-    const uint64_t over = __ballot(upto > r), any = __ballot(t > 0.0);
+    // Sums up to neighbouring chunks are formed in other orders: behind a chunk without weight one may be larger than
+    // before it, by a rounding.  The token lies in a chunk of some weight.
+    const uint64_t any = __ballot(t > 0.0), over = __ballot(upto > r) & any;
     if (over) {
       const int l = __builtin_ctzll(over);
       chunk = i + l;
