@@ -266,7 +266,8 @@ void decode_kernel(DecodeParams p, OrderArg<ORD> ord) {
   // in order): the active flag and the current token first, so that the token can be
   // quantised while the state codes and the buffered tokens are still in flight.
   // branch-free: without a mask the load reads an in-bounds stand-in and is ignored
-  const uint8_t mask_v = *(p.mask ? p.mask + b : (const uint8_t*)countp);
+  // (of a commit: a word a tile)
+  const uint8_t mask_v = *(p.mask ? p.mask + (p.flush_only == 2 ? 4 * ((size_t)b * p.Hv + h) + kFilledByte : b) : (const uint8_t*)countp);
   const bool active = !p.mask || mask_v != 0;
   // current token (a flush-only launch is given in-bounds stand-in pointers)
   const int te = tid < D ? tid : D - 1;
@@ -317,8 +318,8 @@ void decode_kernel(DecodeParams p, OrderArg<ORD> ord) {
     zp_reg = ld_state<NTS>((const uint4*)(asym ? (const uint8_t*)g_zeros : (const uint8_t*)g_scales) + min(tid, zp_vec - 1));
   }
 
-  // counts outside [0, dP) (dP: only between the launches of a commit) cannot come from this library; clamp so that every slot
-  // index stays inside the buffer whatever the buffer holds
+  // counts outside [0, dP) cannot come from this library (dP: between the launches of a commit, for the tiles that it
+  // marks); clamp so that every slot index stays inside the buffer whatever the buffer holds
   const int n0 = min(max(count_raw, 0), p.flush_only == 2 ? p.dP : p.dP - 1);
   const int n = flush_only ? n0 : n0 + 1;
   const bool do_flush = flush_only || n >= p.dP;
@@ -386,8 +387,7 @@ void decode_kernel(DecodeParams p, OrderArg<ORD> ord) {
   // Inactive tiles (and flushes of an empty buffer) leave here, after the barrier: an
   // exit before it would hold every load back until the flag and the count have arrived.
   // Both are uniform over the workgroup, so the whole tile leaves together.
-  // (nothing buffered, or not all of a period where that is asked for: nothing to flush)
-  if (!active || (flush_only && count_raw < (p.flush_only == 2 ? p.dP : 1))) return;
+  if (!active || (flush_only && count_raw <= 0)) return;   // (nothing buffered: nothing to flush)
   if (!flush_only) {
     float Mk = sm.red[0][0], Mv = sm.red[1][0], Mq = sm.red[2][0];
 #pragma unroll

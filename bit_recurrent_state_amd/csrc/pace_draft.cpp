@@ -93,7 +93,7 @@ pace_status pace_draft_commit(const pace_layer_cfg* cfg, void* state, void* buff
   p.most = most;
   // Tokens up to the end of the period, the fold of the buffers that it fills, and on.  At most dP - 1 tokens
   // are held before, so `most` more end at most ceil(most / dP) periods.
-  const DecodeParams fold = flush_params(cfg, state, buffer, 2);
+  DecodeParams fold = flush_params(cfg, state, buffer, 2);
   const int rounds = rounds_of(cfg, most);
   const size_t each = (size_t)cfg->B * cfg->Hv;
   for (int r = 0; r <= rounds; ++r) {
@@ -101,6 +101,7 @@ pace_status pace_draft_commit(const pace_layer_cfg* cfg, void* state, void* buff
     p.done_out = (int32_t*)workspace + r * each;
     if (launch_draft_append(p, cfg->dk, cfg->buf_kind, (hipStream_t)stream) != hipSuccess) return PACE_EHIP;
     if (r == rounds) break;
+    fold.mask = (const uint8_t*)p.done_out;
     if (launch_decode(fold, nullptr, cfg->dk, cfg->dv, cfg->buf_kind, (hipStream_t)stream) != hipSuccess) return PACE_EHIP;
   }
   return PACE_OK;

@@ -2,7 +2,7 @@
 //
 // One workgroup per (sequence, value head) takes the head's share of the path: tokens in D / 8 lanes each, 8 channels a lane,
 // through the buffer quantiser and into the slots from the head's count on, up to the end of the period.  The rounding
-// of the buffers that are then full is the decode kernel's own fold, launched after this one; a further launch of
+// of the buffers that this fills is the decode kernel's own fold, launched after this one; a further launch of
 // this one goes on with the tokens that are left.  Bound by latency: counts -> nodes -> tokens -> slots.
 //
 // Measured, 64 sequences of up to 8 tokens, 32/16 heads of 128: launches of 4.9 us, 3.5 (fold) and 2.3 (mostly
@@ -27,14 +27,14 @@ __global__ __launch_bounds__(kThreads) void append_kernel(CommitParams p) {
   const size_t bh = (size_t)b * l.Hv + h;
   int32_t* const countp = (int32_t*)l.buffer + bh;
   const int n = min(max(*countp, 0), l.dP - 1);
-  const int done = p.done ? p.done[bh] : 0;
+  const int done = p.done ? p.done[bh] & kTakenMask : 0;
   int m = min(max(p.counts[b], 0), p.most);
   // the path ends at its first index that is no node (T <= 64: one lane each)
   const int node_l = lane < p.T ? p.nodes[(size_t)b * p.T + lane] : -1;
   const uint64_t bad = __ballot(lane < m && (node_l < 0 || node_l >= p.T));
   if (bad) m = min(m, __builtin_ctzll(bad));
   const int take = min(m - done, l.dP - n);
-  if (tid == 0) p.done_out[bh] = done + max(take, 0);
+  if (tid == 0) p.done_out[bh] = (done + max(take, 0)) | (take > 0 && n + take == l.dP ? kFilled : 0);
   if (take <= 0) return;
 
   const int c0 = 8 * (tid % LANES);

@@ -31,7 +31,7 @@ struct CommitParams {
   DecodeParams l;               // the layer; k, v, a, beta [B][T]..
   const int32_t* nodes;         // [B][T]
   const int32_t* counts;
-  const int32_t* done;          // [B][Hv] tokens that earlier rounds took (null: none)
+  const int32_t* done;          // [B][Hv] tokens that earlier rounds took (null: none), as kFilled says
   int32_t* done_out;            // [B][Hv]
   int32_t T, most;
 };

@@ -60,6 +60,10 @@ inline BufferLayout buffer_layout(const pace_layer_cfg& c) {
   return L;
 }
 
+// A commit's word of a (sequence, value head): the tokens that it has taken so far, and byte kFilledByte is 1 where its
+// last launch filled the buffer.
+constexpr int kFilledByte = 3, kFilled = 1 << (8 * kFilledByte), kTakenMask = kFilled - 1;
+
 // Everything a decode / flush launch needs, passed to the kernel by value.
 struct DecodeParams {
   uint8_t* state;
@@ -77,7 +81,8 @@ struct DecodeParams {
   uint64_t seq_stride;
   uint64_t off_kc, off_ks, off_v, off_vs, off_a, off_beta;  // buffer regions
   int32_t B, Hv, Hk, gamma, dP, group, asym;
-  int32_t flush_only;   // 1: pace_flush_requant (no new token); 2: only buffers that hold dP tokens
+  int32_t flush_only;   // 1: pace_flush_requant (no new token); 2: only the tiles that a commit marks, whose buffers hold dP
+                        // tokens (mask: its words [B][Hv], of which byte kFilledByte says so)
   int32_t io_bf16;      // q, k, v, o are bf16 (else fp32)
   int32_t bf16_state;   // the state is bf16 values (one dv x dk record per head)
 };
