@@ -12,7 +12,9 @@
 //   Gram         k_j . k_i and k_j . q_i on the bf16 matrix cores, times the decays
 //   projections  tokens (A) times state columns (B), 32 keys an instruction.  A 4-bit code c becomes the bf16 number 16 + c by
 //                a shift and a mask-and-or of two codes; the offset and the zero point are taken off by the tokens' block
-//                sums.  One scale a (column, 32 keys).
+//                sums.  In fp32 codes enter less their zero points: an offset is rounded at its own size, which
+//                outputs in bf16 do not show, but 64 chains of 8 were off by 4.5e-7 of their norm in fp32, now 1.5e-7, in
+//                the same 21.1 us.  One scale a (column, 32 keys).
 //   solve        16 tokens at a time in the matrix unit's layout (4 tokens x 4 columns a lane), four at a time within them
 // Queries enter as they are in bf16, as three bf16 pieces (exact) in fp32.  Everything else is fp32.
 //
@@ -402,7 +404,7 @@ void step_kernel(DraftParams p) {
         const int odd = (KPS > 1 ? tid * (KB / KPS) + kb : tid * (KB >> wide) + (kb >> wide)) & 1;   // (4 bits: two zero points a byte)
         const int zp = is8 ? column_z[kb] : (column_z[kb] >> (4 * odd)) & 15;
         const float z = asym ? (float)zp : (float)(1 << (bits - 1));
-        sm.m.s.z[kb][tid] = (uint16_t)two_bf16(-((is8 ? 0.f : 16.f) + z), 0.f);
+        sm.m.s.z[kb][tid] = (uint16_t)two_bf16(-((!BF16 || is8 ? 0.f : 16.f) + z), 0.f);
       }
     }
   }
@@ -410,8 +412,8 @@ void step_kernel(DraftParams p) {
 
   auto operand = [&](const uint16_t* row) { return *(const v8bf*)(row + 8 * qq); };
   // Projections of a tile's keys and queries on the wave's columns: [s] of strip s, tokens 4 qq + r.  What the operand's codes
-  // are too large by comes first: sums of the tokens' 32-key blocks (A) times offset and scale of the columns' blocks
-  // (B), one fp32 product a strip.  Then turns of 32 keys and two strips, a turn's sums scaled while the next one's products are
+  // are too large by comes first (in fp32 nothing): sums of the tokens' 32-key blocks (A) times offset and scale of the columns'
+  // blocks (B), one fp32 product a strip.  Then turns of 32 keys and two strips, a turn's sums scaled while the next one's products are
   // formed; all at once, the operands and sums are some 100 registers more.
   auto project = [&](auto eight_bits, const uint16_t* rows, v4f (&xk)[SPW], v4f (&xq)[SPW]) {
     constexpr bool E8 = decltype(eight_bits)::value;
@@ -445,7 +447,10 @@ void step_kernel(DraftParams p) {
       }
       return;
     }
-    {
+    if constexpr (!BF16) {
+#pragma unroll
+      for (int s = 0; s < SPW; ++s) xk[s] = xq[s] = none;
+    } else {
       constexpr uint32_t one = 0x3F803F80u;
       const v8bf ones = as_operand(one, one, one, one);
       float sum_k = 0.f, sum_q = 0.f;          // of token l16's block qq
@@ -471,7 +476,7 @@ void step_kernel(DraftParams p) {
       }
     }
     v4f ak[2][2], aq[2][2];                    // [turn][strip of the pair]
-    uint32_t sc[2];
+    uint32_t sc[2], zp = 0u;
     auto add = [&](int turn) {
       const int s0 = 2 * (turn % PAIRS);
 #pragma unroll
@@ -506,12 +511,24 @@ void step_kernel(DraftParams p) {
 #pragma unroll
         for (int i = 0; i < (E8 ? 2 : 1) * KPS; ++i) asm volatile("" : "+v"(raw[s][E8 ? 2 * kb0 + i : kb0 + i]));
       sc[turn & 1] = *(const uint32_t*)&sm.m.s.s[kb0 / KPS][c0 + s0];
+      if constexpr (!BF16) zp = *(const uint32_t*)&sm.m.s.z[kb0][c0 + s0];
 #pragma unroll
       for (int kb = kb0; kb < kb0 + KPS; ++kb)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           v8bf st;
-          if constexpr (E8) {
+          if constexpr (!BF16) {
+            const float z = bits_f32(s ? zp & 0xFFFF0000u : zp << 16);
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t y = E8 ? raw[s0 + s][2 * kb + e] : (raw[s0 + s][kb] >> (4 * e)) & 0x0F0F0F0Fu;
+              asm volatile("" : "+v"(y));      // (bytes from here on: one operation takes and converts one)
+              w[2 * e] = two_bf16((float)(y & 255u) + z, (float)((y >> 16) & 255u) + z);
+              w[2 * e + 1] = two_bf16((float)((y >> 8) & 255u) + z, (float)(y >> 24) + z);
+            }
+            st = as_operand(w[0], w[1], w[2], w[3]);
+          } else if constexpr (E8) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
