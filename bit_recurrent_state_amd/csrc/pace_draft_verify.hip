@@ -365,7 +365,6 @@ __device__ inline void go_on(const VerifyParams& p, Shared<NODES>& s, int b, int
     __syncthreads();
     if (tid < 64) walk(s, len, p.draft != nullptr, tid);
     __syncthreads();
-    if (!s.w.sum && waited && s.w.A > 0.0) break;      // refused no more: the sums stand
     total = row_sums(p, row_of<E>(p, b, s.w, s.gone), sums);
     if (!s.w.sum) break;
   }
