@@ -153,10 +153,6 @@ class VerifyConfig:
     def _c(self):
         return _VerifyCfg(self.B, self.T, self.V, IO_BF16 if self.bf16_probs else IO_F32)
 
-    @cached_property
-    def _bytes(self):
-        return draft_verify_workspace_bytes(self)
-
 
 def draft_verify_workspace_bytes(cfg: VerifyConfig) -> int:
     out = ctypes.c_size_t(0)
@@ -185,6 +181,8 @@ def _probs(t, name, dtype, cfg):
 
 
 def _verify_args(cfg, target, tokens, parents, uniforms, nodes, counts, next_tokens, draft, draft_lens, workspace, stream):
+    if workspace is None:
+        raise ValueError("workspace is required: uint8 of draft_verify_workspace_bytes(cfg)")
     dtype = torch.bfloat16 if cfg.bf16_probs else torch.float32
     tp, ts = _probs(target, "target", dtype, cfg)
     dp, ds = _probs(draft, "draft", dtype, cfg) if draft is not None else (None, 0)
@@ -198,15 +196,15 @@ def _verify_args(cfg, target, tokens, parents, uniforms, nodes, counts, next_tok
             _ptr(parents, "parents", i32, optional=True), step, _at(uniforms, "uniforms", torch.float32, n),
             _ptr(draft_lens, "draft_lens", i32, cfg.B, optional=True), _at(nodes, "nodes", i32, n),
             _at(counts, "counts", i32, cfg.B), _at(next_tokens, "next_tokens", i32, cfg.B),
-            _ptr(workspace, "workspace", torch.uint8, optional=True),
-            workspace.numel() if workspace is not None else 0, _stream(stream))
+            _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
 
 
 def draft_verify(cfg: VerifyConfig, target, tokens, parents, uniforms, nodes, counts, next_tokens, draft=None,
                  draft_lens=None, workspace=None, stream=None):
     """pace_draft_verify.  target, draft [B, T, V] (rows may be slices of longer ones; draft None: children were not
     drawn from probabilities); tokens int32 [B, T]; parents int32 [B or 1, T] (None: a chain); uniforms fp32 [B, T];
-    out: nodes int32 [B, T], counts and next_tokens int32 [B]; workspace uint8 of draft_verify_workspace_bytes(cfg)."""
+    out: nodes int32 [B, T], counts and next_tokens int32 [B]; workspace uint8 of draft_verify_workspace_bytes(cfg), which every
+    call needs."""
     _call(LIB.pace_draft_verify, "pace_draft_verify",
           _verify_args(cfg, target, tokens, parents, uniforms, nodes, counts, next_tokens, draft, draft_lens, workspace, stream))
 
