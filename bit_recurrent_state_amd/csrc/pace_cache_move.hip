@@ -17,6 +17,7 @@
 
 #include "pace_cache_internal.h"
 #include "pace_draft_internal.h"
+#include "pace_move_range.h"
 
 namespace pace {
 namespace {
@@ -72,11 +73,9 @@ __device__ inline void walk(const MoveParams& p, const Layout& y, int piece, int
   constexpr int STEP = NT / KL;                // tokens a step
   __shared__ int64_t from[4][STEP], to[4][STEP];
   const int tid = threadIdx.x, b = blockIdx.y;
-  const int64_t start = p.start[b];
-  const int count = min(max(p.counts[b], 0), p.T);
-  const int64_t end = min(start + count, (int64_t)p.max_pages << p.page_shift);
-  const int64_t base = max(start, (int64_t)0) & ~(int64_t)15;
-  if (max(start, (int64_t)0) >= end) return;   // (from here on count > 0: there is a node to read)
+  MoveRange range;
+  if (!move_range(p.start[b], p.counts[b], p.T, (int64_t)p.max_pages << p.page_shift, range)) return;
+  const int64_t start = range.start, end = range.end, base = range.base;
   const int steps = (int)((end - base + STEP - 1) / STEP);
   const int32_t* const nodes = p.nodes + b * p.nodes_stride;
   const int32_t* const src_table = p.src_table + (int64_t)b * p.max_pages;
@@ -87,7 +86,7 @@ __device__ inline void walk(const MoveParams& p, const Layout& y, int piece, int
   // The entry that destination mine + s STEP takes, in three parts a step apart: its node, its pages, its place.
   auto entry = [&](int64_t pos) { return (int)min(max(pos >> p.page_shift, (int64_t)0), (int64_t)p.max_pages - 1); };
   auto load_node = [&](int s, int& node) {
-    if (tid < STEP) node = nodes[min(max(mine + (int64_t)s * STEP - start, (int64_t)0), (int64_t)count - 1)];
+    if (tid < STEP) node = nodes[node_place(range, mine + (int64_t)s * STEP)];
   };
   struct Pages {
     int node, from, to;
