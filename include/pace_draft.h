@@ -47,8 +47,8 @@ extern "C" {
  * Rows have to be paths: with bit j, row i has the bits of row j.  (Others give numbers, of the sums that the bits say.)
  * No rounding of the state falls between drafts: a path that passes the end of the decode period sees
  * the state as it stands, and is rounded when it is committed.
- * draft_lens int32 [B] (device, NULL = T): sequence b has draft_lens[b] tokens; what lies behind them is not
- * read, and their o is 0.
+ * draft_lens int32 [B] (device, NULL = T): sequence b has draft_lens[b] tokens; rows behind them may hold anything (they
+ * may be loaded, but no result depends on them), and their o is 0.
  * q, k [B][T][Hk][dk];  v, o [B][T][Hv][dv];  a, beta fp32 [B][T][Hv], contiguous, 16-byte aligned
  * (a, beta: 4-byte).  o must not overlap an input.
  * Every state and buffer kind of pace.h; keys enter as exact codes, products and sums are fp32.
@@ -93,7 +93,7 @@ typedef struct {
  *
  * target [B][T][V]: row i holds the probabilities of the token after node i.  draft [B][T][V]: row i
  * the probabilities from which the children of node i were drawn, independently; NULL: the children were not drawn (the
- * likeliest tokens, a lookup).  tokens int32 [B][T]: the nodes' tokens (node 0's is not read).
+ * likeliest tokens, a lookup).  tokens int32 [B][T]: the nodes' tokens (node 0's may be anything).
  * parents int32: parents[b * parents_stride + i], NULL: a chain (parents_stride in elements, 0: one tree for all sequences); a
  * node whose parent is not in [0, i) is nobody's child.  uniforms fp32 [B][T] in [0, 1): [0] draws the following token,
  * [i] decides on node i.  draft_lens int32 [B] (NULL = T): only nodes below it count; 0: a sequence with nothing to verify.
