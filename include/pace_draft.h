@@ -15,7 +15,9 @@
  *
  * The conventions are those of pace.h and pace_cache.h: plain C, caller-owned device memory,
  * host-side validation before any launch (PACE_EINVAL / PACE_EUNSUPPORTED, nothing touched),
- * launch errors as PACE_EHIP, no global state, no allocation and no synchronisation.  Every
+ * launch errors as PACE_EHIP, no global state, no allocation and no synchronisation.  A call of several launches ends
+ * at the first error, and what it writes is then lost: pace_draft_commit may leave a layer's buffer full and not yet
+ * folded, which no other call takes for what it is, so the layer's state and buffer have to be set up anew.  Every
  * call only enqueues kernels on `stream` (a hipStream_t, NULL = default stream).  Memory handed to a
  * call, its workspace among it, must not be used by other work until the call's kernels have run:
  * calls that may overlap (other streams, other graphs) need workspaces of their own.
