@@ -36,8 +36,10 @@ namespace pace {
 namespace {
 
 // Waves of a workgroup: two where one tile holds all tokens (eight such workgroups a compute unit), four beyond it
-// (LDS leaves four, or fewer).  64 chains of 8 in two waves 15.2 us, in four 17.0 (one sequence's five: 6.0 and 5.4); 16 trees
-// of 25 in two 17.8 us, in four 14.1.
+// (LDS leaves four, or fewer).  32/16 heads of 128, in a graph, in two waves and in four: 64 chains of 8 14.0 and 15.8 us, 32 9.6
+// and 10.0, 16 7.5 and 6.6, one sequence's five 5.6 and 5.0; 16 trees of 25 16.9 and 13.4.  (Four for one tile of few
+// sequences would be one more kernel of each kind for those 10%.)  At d = 64 each of four waves would have one strip of
+// columns, and strips are taken in pairs.
 template <int D, int NKT>
 constexpr int waves_of() {
   return NKT == 1 || D == 64 ? 2 : 4;
@@ -730,7 +732,8 @@ hipError_t launch(const DraftParams& p, int buf_kind, hipStream_t s) {
     step_kernel<D, NKT, BF16, false, 4, 1, true><<<grid, kThreads, 0, s>>>(p);
   } else if (BF16 && p.l.mask8 == 0 && !mixed && p.l.group == 64) {
     // All heads in 4 bits, the symmetric layout's groups: fewer registers, no second way through the projections, half
-    // as many scalings.  When it was added, 64 x 8 drafts took 15.5 us, by the general kernel 16.1; one sequence's five 6.4 and 6.8.
+    // as many scalings.  64 chains of 8 take 14.0 us, by the general kernel 14.8; one sequence's five 5.6 and 6.1.  (The
+    // layout that batches are served in; not tried for fp32, the mixed buffer or some heads in 8 bits.)
     if constexpr (BF16) step_kernel<D, NKT, true, false, 4, 2, false><<<grid, kThreads, 0, s>>>(p);
   } else if (mixed) {
     step_kernel<D, NKT, BF16, true, 0, 1, false><<<grid, kThreads, 0, s>>>(p);
@@ -742,7 +745,7 @@ hipError_t launch(const DraftParams& p, int buf_kind, hipStream_t s) {
 
 template <int D, bool BF16>
 hipError_t by_tiles(const DraftParams& p, int buf_kind, hipStream_t s) {
-  // (LDS goes by the tiles: 64 chains of 8 in the one tile that they need 14.8 us, in the kernel for two 17.9)
+  // (LDS goes by the tiles: 64 chains of 8 in the one tile that they need 14.0 us, in the kernel for two 17.6)
   const int t = draft_tiles(p.l.dP, p.T);
   if (t <= 1) return launch<D, 1, BF16>(p, buf_kind, s);
   if (t <= 2) return launch<D, 2, BF16>(p, buf_kind, s);

@@ -439,8 +439,9 @@ template <typename E, int NODES>
 void launch(const VerifyParams& p, hipStream_t s) {
   // Two kernels where one workgroup a sequence leaves much of the chip idle for long: few sequences, rows of more than a chunk a
   // wave.  Chains of 8, drawn, fp32, in one kernel and in two: V = 131072: 1 sequence 21.5 and 8.1 us, 64 28.3 and 18.9, 128
-  // 35.3 and 31.5, 192 45.0 and 47.8; V = 65536: 16 14.5 and 10.4, 256 28.3 and 30.7; V = 32768: 1 sequence 9.4 and 8.0 in a
-  // graph, but 9.4 and 11.6 called eagerly (a second launch), 32 10.2 and 10.4, 128 12.6 and 14.3.
+  // 35.3 and 31.5, 192 45.0 and 47.8; V = 65536: 16 14.5 and 10.4, 256 28.3 and 30.7; V = 32768: 32 10.2 and 10.4, 128 12.6 and
+  // 14.3.  One chain of 5 over 32768: 9.5 and 8.0 in a graph, 9.8 and 11.1 to 12.9 called eagerly: a second launch costs an eager
+  // call as much as it saves a captured one, or more, and from few sequences on it saves nothing there.
   if (p.chunks <= kWaves || p.B > std::min(2 * p.chunks, 128)) {
     verify_kernel<E, NODES><<<p.B, kThreads, 0, s>>>(p);
     return;
@@ -454,7 +455,7 @@ void launch(const VerifyParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_draft_verify(const VerifyParams& p, int prob_bf16, hipStream_t stream) {
-  // (LDS for 64 nodes or for 1024: 64 chains of 8 over 131072 tokens 18.8 us, with the larger 22.2)
+  // (LDS for 64 nodes or for 1024: 64 chains of 8 over 131072 tokens 18.9 us, with the larger 22.2)
   if (p.T <= 64) {
     if (prob_bf16) launch<uint16_t, 64>(p, stream);
     else launch<float, 64>(p, stream);
