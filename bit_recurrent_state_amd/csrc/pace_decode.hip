@@ -266,8 +266,7 @@ void decode_kernel(DecodeParams p, OrderArg<ORD> ord) {
   // in order): the active flag and the current token first, so that the token can be
   // quantised while the state codes and the buffered tokens are still in flight.
   // branch-free: without a mask the load reads an in-bounds stand-in and is ignored
-  // (of a commit: a word a tile)
-  const uint8_t mask_v = *(p.mask ? p.mask + (p.flush_only == 2 ? 4 * ((size_t)b * p.Hv + h) + kFilledByte : b) : (const uint8_t*)countp);
+  const uint8_t mask_v = *(p.mask ? p.mask + b : (const uint8_t*)countp);
   const bool active = !p.mask || mask_v != 0;
   // current token (a flush-only launch is given in-bounds stand-in pointers)
   const int te = tid < D ? tid : D - 1;
@@ -387,7 +386,10 @@ void decode_kernel(DecodeParams p, OrderArg<ORD> ord) {
   // Inactive tiles (and flushes of an empty buffer) leave here, after the barrier: an
   // exit before it would hold every load back until the flag and the count have arrived.
   // Both are uniform over the workgroup, so the whole tile leaves together.
-  if (!active || (flush_only && count_raw <= 0)) return;   // (nothing buffered: nothing to flush)
+  // (nothing buffered, or not all of a period where that is asked for: nothing to flush)
+  if (!active || (flush_only && count_raw < (p.flush_only == 2 ? p.dP : 1))) return;
+  // (a count of dP or more that the commit found, not one that it made)
+  if (p.flush_only == 2 && !(p.filled[(size_t)b * p.Hv + h] & kFilled)) return;
   if (!flush_only) {
     float Mk = sm.red[0][0], Mv = sm.red[1][0], Mq = sm.red[2][0];
 #pragma unroll

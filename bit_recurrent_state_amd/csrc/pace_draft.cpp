@@ -101,7 +101,7 @@ pace_status pace_draft_commit(const pace_layer_cfg* cfg, void* state, void* buff
     p.done_out = (int32_t*)workspace + r * each;
     if (launch_draft_append(p, cfg->dk, cfg->buf_kind, (hipStream_t)stream) != hipSuccess) return PACE_EHIP;
     if (r == rounds) break;
-    fold.mask = (const uint8_t*)p.done_out;
+    fold.filled = p.done_out;
     if (launch_decode(fold, nullptr, cfg->dk, cfg->dv, cfg->buf_kind, (hipStream_t)stream) != hipSuccess) return PACE_EHIP;
   }
   return PACE_OK;

@@ -60,9 +60,9 @@ inline BufferLayout buffer_layout(const pace_layer_cfg& c) {
   return L;
 }
 
-// A commit's word of a (sequence, value head): the tokens that it has taken so far, and byte kFilledByte is 1 where its
-// last launch filled the buffer.
-constexpr int kFilledByte = 3, kFilled = 1 << (8 * kFilledByte), kTakenMask = kFilled - 1;
+// A commit's word of a (sequence, value head): the tokens that it has taken so far, and kFilled where its last launch
+// filled the buffer.
+constexpr int32_t kFilled = 1 << 24, kTakenMask = kFilled - 1;
 
 // Everything a decode / flush launch needs, passed to the kernel by value.
 struct DecodeParams {
@@ -75,14 +75,14 @@ struct DecodeParams {
   const float* beta;
   const uint8_t* mask;  // active (decode) or seq_mask (flush); may be null
   void* o;
+  const int32_t* filled;  // flush_only = 2: the commit's words [B][Hv]
   uint64_t mask8;       // bit h set: head h is 8-bit
   uint32_t rec4, rec8;  // record bytes of 4-bit / 8-bit heads
   uint32_t scales_off4, zeros_off4, scales_off8, zeros_off8;  // offsets inside a record
   uint64_t seq_stride;
   uint64_t off_kc, off_ks, off_v, off_vs, off_a, off_beta;  // buffer regions
   int32_t B, Hv, Hk, gamma, dP, group, asym;
-  int32_t flush_only;   // 1: pace_flush_requant (no new token); 2: only the tiles that a commit marks, whose buffers hold dP
-                        // tokens (mask: its words [B][Hv], of which byte kFilledByte says so)
+  int32_t flush_only;   // 1: pace_flush_requant (no new token); 2: only buffers that a commit filled (with dP tokens)
   int32_t io_bf16;      // q, k, v, o are bf16 (else fp32)
   int32_t bf16_state;   // the state is bf16 values (one dv x dk record per head)
 };
