@@ -5,9 +5,9 @@
 // of the buffers that this fills is the decode kernel's own fold, launched after this one; a further launch of
 // this one goes on with the tokens that are left.  Bound by latency: counts -> nodes -> tokens -> slots.
 //
-// Measured, 64 sequences of up to 8 tokens, 32/16 heads of 128: launches of 4.9 us, 3.5 (fold) and 2.3 (mostly
-// nothing left), 11.1 us together in a graph; a launch that finds nothing to do takes 2.3.  Fewer launches would need the
-// value heads of a key head to wait for one another, since they share its key slots.
+// Measured, 64 sequences of up to 8 tokens, 32/16 heads of 128: launches of 5.0 us, 3.6 (fold) and 2.4 (mostly
+// nothing left), 11.4 us together in a graph, 24.5 where every sequence ends its period; a launch that finds nothing to do takes
+// 2.4.  Tokens of the next period need a launch behind the fold, since the value heads of a key head share its key slots.
 #include <hip/hip_runtime.h>
 
 #include "pace_draft_internal.h"

@@ -8,8 +8,7 @@
 // so the state of no node is ever formed: the tile's codes are read once, for all tokens.
 //
 //   tokens       buffered codes and quantised drafts as bf16 (exact) in LDS, in the order of the state's units
-//   decays       row i's products by one lane, walking its path back
-//   Gram         k_j . k_i and k_j . q_i on the bf16 matrix cores, times the decays
+//   Gram         k_j . k_i and k_j . q_i on the bf16 matrix cores, times the decays: products along i's path, from its end back
 //   projections  tokens (A) times state columns (B), 32 keys an instruction.  A 4-bit code c becomes the bf16 number 16 + c by
 //                a shift and a mask-and-or of two codes; the offset and the zero point are taken off by the tokens' block
 //                sums.  In fp32 codes enter less their zero points: an offset is rounded at its own size, which
@@ -18,7 +17,7 @@
 //   solve        16 tokens at a time in the matrix unit's layout (4 tokens x 4 columns a lane), four at a time within them
 // Queries enter as they are in bf16, as three bf16 pieces (exact) in fp32.  Everything else is fp32.
 //
-// Measured (graph), 32/16 heads of 128, int4 state: 64 chains of up to 8 14.15 us, 2.1 TB/s (a large copy: 5.1).  All 2048
+// Measured (graph), 32/16 heads of 128, int4 state: 64 chains of up to 8 14.0 us, 2.1 TB/s (a large copy: 5.1).  All 2048
 // workgroups are on the chip at once: their loads take 6 us together, so that the last quarter waits for its tokens, and
 // then takes the 6 us of a workgroup; vector unit and LDS are busy half of the time each, the matrix unit 23%, waves wait for
 // their turn 44% of theirs.  16 trees of up to 25 (mixed heads and buffer): 13.3 us, two workgroups a compute unit, vector
