@@ -2,23 +2,26 @@
 //
 // The probabilities of every node's token in its parent's rows are gathered at once; one wave then walks the tree, 64 nodes
 // a ballot.  With A the sum of the W's so far, what is left of a row after its refused children
-// is w = max(p - A q, 0) (the same as taking W q off each time, as q >= 0), so that a row's state is two numbers.
+// is w = max(p - A q, 0) (the same as taking W q off each time, as q >= 0), so that a row's state is A and W.  Where
+// little is left, A q is nearly p: A is kept whole, in as many doubles as it takes, and w is as good as if W q had been taken off
+// each time.
 // A row is read only where its sum is asked for: after a refusal with the draft's probabilities, and to draw the following
 // token.  It is summed in chunks of 2048 tokens, one a wave; the token is found by the chunks' sums and then inside its
 // chunk.  All in fp64: the fp32 (bf16) inputs are exact.  A weight passes 7 additions in its lane, 6 over the lanes, one for
 // every 64 chunks and 6 over those, so that a sum of 2^24 weights is off by 147 roundings of 2^-53 at most, 2^-45.8 of itself;
-// with the draft's probabilities a weight is besides off by one rounding of A q and one of the difference.
+// with the draft's probabilities a weight is besides off by a rounding for each part of A (one up to two refusals, mostly).
 //
 // Bound by memory for large batches and by latency for small ones.  Measured (graph): 64 chains of 8 over 131072 tokens,
-// fp32, drawn: 18.9 us, of which the sums 14.8 (4.5 TB/s; a large copy 5.1) and the rest 4.2; 16 trees of 25 over
-// 100003 tokens, bf16, not drawn: 10.9 us (7.5 and 4.4): parents -> probabilities -> walk -> row; one chain of 5 over
-// 32768: 9.5 us.
+// fp32, drawn: 18.8 us, of which the sums 14.8 (4.5 TB/s; a large copy 5.1) and the rest 4.0; 16 trees of 25 over
+// 100003 tokens, bf16, not drawn: 10.3 us (7.2 and 4.1): parents -> probabilities -> walk -> row; one chain of 5 over
+// 32768: 9.4 us.
 //
 // Few sequences over a large vocabulary: the first row that is asked for is summed by several workgroups a sequence, each
 // of which walks there by itself; a second kernel goes on from there.  Otherwise one workgroup a sequence does it all.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pace_draft_internal.h"
 #include "pace_numerics.h"
@@ -70,20 +73,26 @@ __device__ inline double wave_scan(double x) {
 }
 __device__ inline double wave_sum(double x) { return lane_double(wave_scan(x), 63); }
 
-// The walk's state, and what of it a second kernel needs.
+// The walk's state, and what of it a second kernel needs (which begins behind one refusal at most: A = 1 without a rest).
 struct Walk {
-  double A, W;
+  double A, W;                           // A and the parts of `rest`
   int32_t x, at, length, ngone;          // the node, the last child looked at, accepted nodes, refused ones (draft NULL)
   int32_t sum, more;                     // the row's sum is waited for; children of x are left behind `at`
+  int32_t parts;                         // of `rest`
 };
 
 static_assert(sizeof(Walk) <= 48, "verify_scratch");
+
+// Parts follow one another by 53 bits or more, down to the smallest double.
+constexpr int kParts = 21;
 
 template <int NODES>
 struct Shared {
   double pt[NODES], qt[NODES], u[NODES]; // of a node's token, in its parent's rows of target and draft; its uniform
   int32_t parent[NODES], token[NODES], path[NODES];
   int32_t gone[NODES];                   // draft NULL: tokens of the refused children of x
+  double rest[kParts];                   // what A has beyond its first 53 bits, the largest part first
+  double part[kParts + 1];               // (at work)
   double sums[kLdsChunks];
   Walk w;
 };
@@ -119,9 +128,47 @@ __device__ inline int begin(const VerifyParams& p, Shared<NODES>& s, int b, cons
     s.u[c] = uniform(u);
     s.path[c] = 0;
   }
-  if (tid == 0) s.w = Walk{0.0, 1.0, 0, 0, 1, 0, 0, 0};
+  if (tid == 0) s.w = Walk{0.0, 1.0, 0, 0, 1, 0, 0, 0, 0};
   __syncthreads();
   return len;
+}
+
+// A sum of two doubles and what its rounding loses, exactly.
+__device__ inline double two_sum(double a, double b, double& lost) {
+  const double s = a + b, t = s - a;
+  lost = (a - (s - t)) + (b - t);
+  return s;
+}
+
+// A + rest[0] + .. + rest[n - 1] gains x, and none of it is lost; the number of parts afterwards.  part: n + 1 at work.
+__device__ inline int gain(double& A, double* rest, int n, double x, double* part) {
+  for (int i = n - 1; i >= 0; --i) x = two_sum(rest[i], x, part[i + 1]);
+  A = two_sum(A, x, part[0]);
+  // each part as large as the ones behind it make it
+  int k = -1;
+  double top = A;
+  for (int i = 0; i <= n; ++i) {
+    double lost;
+    const double s = two_sum(top, part[i], lost);
+    if (lost != 0.0) {
+      if (k < 0) A = s;
+      else rest[k] = s;
+      if (++k == kParts) return kParts;
+      top = lost;
+    } else {
+      top = s;
+    }
+  }
+  if (k < 0) A = top;
+  else if (top != 0.0) rest[k++] = top;
+  return max(k, 0);
+}
+
+// What the refused children leave of p.
+__device__ inline double left(double p, double q, double A, const double* rest, int parts) {
+  double w = fma(-A, q, p);
+  for (int i = 0; i < parts; ++i) w = fma(-rest[i], q, w);
+  return fmax(w, 0.0);
 }
 
 // Goes on with the walk; returns at its end (sum = 0) or where a row's sum is needed (sum = 1).  One wave.
@@ -129,7 +176,7 @@ template <int NODES>
 __device__ inline void walk(Shared<NODES>& s, int len, bool drawn, int lane) {
   int x = s.w.x, at = s.w.at, length = s.w.length, ngone = s.w.ngone;
   double A = s.w.A, W = s.w.W;
-  int sum = 0, more = 0;
+  int sum = 0, more = 0, parts = s.w.parts;
   for (int blk = (at + 1) / 64; blk * 64 < len && !more; ++blk) {
     const int c = blk * 64 + lane;
     const bool in = c < len;
@@ -150,7 +197,7 @@ __device__ inline void walk(Shared<NODES>& s, int len, bool drawn, int lane) {
       bool accept;
       if (drawn) {
         const double q = lane_double(qt, l);
-        w = fmax(w - A * q, 0.0);
+        w = left(w, q, A, s.rest, parts);
         accept = uc * W * q < w;
       } else {
         for (int i = 0; i < ngone; i += 64)
@@ -163,10 +210,10 @@ __device__ inline void walk(Shared<NODES>& s, int len, bool drawn, int lane) {
         ++length;
         A = 0.0;
         W = 1.0;
+        parts = 0;
         ngone = 0;
       } else if (drawn) {
-        A += W;
-        sum = 1;
+        sum = 1;                         // (the last one that this call looks at)
       } else {
         W = fmax(W - w, 0.0);
         if (lane == 0) s.gone[ngone] = t;
@@ -175,7 +222,10 @@ __device__ inline void walk(Shared<NODES>& s, int len, bool drawn, int lane) {
       }
     }
   }
-  if (lane == 0) s.w = Walk{A, W, x, at, length, ngone, sum, more};
+  if (lane == 0) {
+    if (sum) parts = gain(A, s.rest, parts, W, s.part);
+    s.w = Walk{A, W, x, at, length, ngone, sum, more, parts};
+  }
 }
 
 // A row of target, less what was refused of it.
@@ -183,26 +233,45 @@ template <typename E>
 struct Row {
   const E *p, *q;                        // q null: nothing drawn was refused
   double A;
+  const double* rest;
+  int parts;
   const int32_t* gone;
   int ngone, V;
 };
 
-// Weights of eight neighbouring tokens.
-template <typename E>
+// Weights of eight neighbouring tokens.  What a row has decides once for a chunk, so that the loads of all its tokens may be on
+// their way together.
+enum { kWhole, kLess, kLessRest };         // no q; A alone; A with parts beyond it
+
+template <int HAS, typename E>
 __device__ inline void weights(const Row<E>& r, int v0, double (&w)[8]) {
   Eight<E> a, q;
   if (v0 + 8 <= r.V) {
     a = *(const Eight<E>*)(r.p + v0);
-    if (r.q) q = *(const Eight<E>*)(r.q + v0);
+    if constexpr (HAS != kWhole) q = *(const Eight<E>*)(r.q + v0);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       a.v[i] = v0 + i < r.V ? r.p[v0 + i] : E(0);
-      if (r.q) q.v[i] = v0 + i < r.V ? r.q[v0 + i] : E(0);
+      if constexpr (HAS != kWhole) q.v[i] = v0 + i < r.V ? r.q[v0 + i] : E(0);
     }
   }
+  double y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = r.q ? fmax(weight(a.v[i]) - r.A * weight(q.v[i]), 0.0) : weight(a.v[i]);
+  for (int i = 0; i < 8; ++i) {
+    w[i] = weight(a.v[i]);
+    if constexpr (HAS != kWhole) {         // (as `left`)
+      y[i] = weight(q.v[i]);
+      w[i] = fma(-r.A, y[i], w[i]);
+    }
+  }
+  if constexpr (HAS == kLessRest)
+    for (int k = 0; k < r.parts; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = fma(-r.rest[k], y[i], w[i]);
+  if constexpr (HAS != kWhole)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = fmax(w[i], 0.0);
   for (int k = 0; k < r.ngone; ++k) {
     const int d = r.gone[k] - v0;
     if (__any(d >= 0 && d < 8)) {
@@ -212,16 +281,24 @@ __device__ inline void weights(const Row<E>& r, int v0, double (&w)[8]) {
     }
   }
 }
+template <typename E, typename F>
+__device__ inline void by_row(const Row<E>& r, F f) {
+  if (!r.q) f(std::integral_constant<int, kWhole>{});
+  else if (!r.parts) f(std::integral_constant<int, kLess>{});
+  else f(std::integral_constant<int, kLessRest>{});
+}
 
 template <typename E>
 __device__ inline double chunk_sum(const Row<E>& r, int chunk, int lane) {
   double sum = 0.0;
+  by_row(r, [&](auto has) {
 #pragma unroll
-  for (int j = 0; j < kPer / 8; ++j) {
-    double w[8];
-    weights(r, chunk * kVerifyChunk + j * 512 + lane * 8, w);
-    sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-  }
+    for (int j = 0; j < kPer / 8; ++j) {
+      double w[8];
+      weights<decltype(has)::value>(r, chunk * kVerifyChunk + j * 512 + lane * 8, w);
+      sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+    }
+  });
   return wave_sum(sum);
 }
 
@@ -281,7 +358,7 @@ __device__ inline void token_at(const VerifyParams& p, const Row<E>& row, const 
   }
   const int v0 = chunk * kVerifyChunk + wave * 512 + lane * 8;
   double w[8];
-  weights(row, v0, w);
+  by_row(row, [&](auto has) { weights<decltype(has)::value>(row, v0, w); });
   double t = 0.0;
   int high = -1;
 #pragma unroll
@@ -331,9 +408,10 @@ __device__ inline const E* draft_of(const VerifyParams& p, int b) {
   return p.draft ? (const E*)p.draft + (int64_t)b * p.T * p.draft_stride : nullptr;
 }
 template <typename E>
-__device__ inline Row<E> row_of(const VerifyParams& p, int b, const Walk& w, const int32_t* gone) {
+__device__ inline Row<E> row_of(const VerifyParams& p, int b, const Walk& w, const double* rest, const int32_t* gone) {
   const E* const draft = draft_of<E>(p, b);
-  return {target_of<E>(p, b) + w.x * p.target_stride, draft && w.A > 0.0 ? draft + w.x * p.draft_stride : nullptr, w.A, gone, w.ngone, p.V};
+  return {target_of<E>(p, b) + w.x * p.target_stride, draft && w.A > 0.0 ? draft + w.x * p.draft_stride : nullptr, w.A, rest, w.parts,
+          gone, w.ngone, p.V};
 }
 
 // The results from the walk's end.  total: of the row as it is left, chunk by chunk in sums.
@@ -367,10 +445,10 @@ __device__ inline void go_on(const VerifyParams& p, Shared<NODES>& s, int b, int
     __syncthreads();
     if (tid < 64) walk(s, len, p.draft != nullptr, tid);
     __syncthreads();
-    total = row_sums(p, row_of<E>(p, b, s.w, s.gone), sums);
+    total = row_sums(p, row_of<E>(p, b, s.w, s.rest, s.gone), sums);
     if (!s.w.sum) break;
   }
-  finish(p, b, s.w, s.path, row_of<E>(p, b, s.w, s.gone), sums, total);
+  finish(p, b, s.w, s.path, row_of<E>(p, b, s.w, s.rest, s.gone), sums, total);
 }
 
 // A sequence without drafts.
@@ -403,7 +481,8 @@ __global__ __launch_bounds__(kSumThreads) void sums_kernel(VerifyParams p) {
   if (tid < 64) walk(s, len, p.draft != nullptr, tid);
   __syncthreads();
   const Scratch to = scratch_of(p, b);
-  const Row<E> row = row_of<E>(p, b, s.w, s.gone);
+  Row<E> row = row_of<E>(p, b, s.w, s.rest, s.gone);
+  row.parts = 0;                         // (one refusal: A is 1)
   const int waves = gridDim.x * (kSumThreads / 64);
   for (int i = blockIdx.x * (kSumThreads / 64) + tid / 64; i < p.chunks; i += waves) {
     const double t = chunk_sum(row, i, tid & 63);
@@ -425,7 +504,9 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(VerifyParams p) {
   if (p.draft_lens && p.draft_lens[b] <= 0) return nothing(p, b);
   const double total = total_of(from.sums, p.chunks, tid & 63);
   if (!w.more) {
-    finish(p, b, w, from.path, row_of<E>(p, b, w, from.gone), from.sums, total);
+    Row<E> row = row_of<E>(p, b, w, nullptr, from.gone);
+    row.parts = 0;                       // (one refusal: A is 1)
+    finish(p, b, w, from.path, row, from.sums, total);
     return;
   }
   const int len = begin(p, s, b, target_of<E>(p, b), draft_of<E>(p, b));
@@ -438,9 +519,9 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(VerifyParams p) {
 template <typename E, int NODES>
 void launch(const VerifyParams& p, hipStream_t s) {
   // Two kernels where one workgroup a sequence leaves much of the chip idle for long: few sequences, rows of more than a chunk a
-  // wave.  Chains of 8, drawn, fp32, in one kernel and in two: V = 131072: 1 sequence 21.5 and 8.1 us, 64 28.3 and 18.9, 128
+  // wave.  Chains of 8, drawn, fp32, in one kernel and in two: V = 131072: 1 sequence 21.5 and 8.1 us, 64 28.3 and 18.8, 128
   // 35.3 and 31.5, 192 45.0 and 47.8; V = 65536: 16 14.5 and 10.4, 256 28.3 and 30.7; V = 32768: 32 10.2 and 10.4, 128 12.6 and
-  // 14.3.  One chain of 5 over 32768: 9.5 and 8.0 in a graph, 9.8 and 11.1 to 12.9 called eagerly: a second launch costs an eager
+  // 14.3.  One chain of 5 over 32768: 9.4 and 8.0 in a graph, 9.8 and 11.1 to 12.9 called eagerly: a second launch costs an eager
   // call as much as it saves a captured one, or more, and from few sequences on it saves nothing there.
   if (p.chunks <= kWaves || p.B > std::min(2 * p.chunks, 128)) {
     verify_kernel<E, NODES><<<p.B, kThreads, 0, s>>>(p);
@@ -455,7 +536,7 @@ void launch(const VerifyParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_draft_verify(const VerifyParams& p, int prob_bf16, hipStream_t stream) {
-  // (LDS for 64 nodes or for 1024: 64 chains of 8 over 131072 tokens 18.9 us, with the larger 22.2)
+  // (LDS for 64 nodes or for 1024: 64 chains of 8 over 131072 tokens 18.8 us, with the larger 22.2)
   if (p.T <= 64) {
     if (prob_bf16) launch<uint16_t, 64>(p, stream);
     else launch<float, 64>(p, stream);
