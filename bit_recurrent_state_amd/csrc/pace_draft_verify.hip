@@ -12,8 +12,8 @@
 // with the draft's probabilities a weight is besides off by a rounding for each part of A (one up to two refusals, mostly).
 //
 // Bound by memory for large batches and by latency for small ones.  Measured (graph): 64 chains of 8 over 131072 tokens,
-// fp32, drawn: 18.8 us, of which the sums 14.8 (4.5 TB/s; a large copy 5.1) and the rest 4.0; 16 trees of 25 over
-// 100003 tokens, bf16, not drawn: 10.3 us (7.2 and 4.1): parents -> probabilities -> walk -> row; one chain of 5 over
+// fp32, drawn: 18.8 us, of which the sums 14.7 (4.6 TB/s; a large copy 5.1) and the rest 4.1; 16 trees of 25 over
+// 100003 tokens, bf16, not drawn: 10.3 us (7.4 and 4.3 by themselves): parents -> probabilities -> walk -> row; one chain of 5 over
 // 32768: 9.4 us.
 //
 // Few sequences over a large vocabulary: the first row that is asked for is summed by several workgroups a sequence, each
